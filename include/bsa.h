@@ -71,7 +71,11 @@ enum { BSA_SCORE_PREFILL = 0, BSA_SCORE_DECODE = 1, BSA_SCORE_GIST = 2, BSA_SCOR
 /* candidate rules for bsa_topk_select */
 enum { BSA_TOPK_CAUSAL_BLOCK = 0, BSA_TOPK_LAST_BLOCK = 1, BSA_TOPK_PLAIN = 2 };
 /* operations for bsa_workspace_bytes */
-enum { BSA_OP_DECODE = 0, BSA_OP_GIST_DECODE = 1, BSA_OP_DECODE_HEADS = 2 };
+enum { BSA_OP_DECODE = 0, BSA_OP_GIST_DECODE = 1, BSA_OP_DECODE_HEADS = 2, BSA_OP_DECODE_QUANT = 3 };
+/* rotation layouts: none; channel i with i + rot_dim/2; channel 2i with 2i + 1 */
+enum { BSA_ROPE_NONE = 0, BSA_ROPE_HALF = 1, BSA_ROPE_PAIRS = 2 };
+/* frequency scalings for bsa_rope_inv_freq */
+enum { BSA_ROPE_PLAIN = 0, BSA_ROPE_LINEAR = 1, BSA_ROPE_BASE = 2, BSA_ROPE_PARTS = 3 };
 
 /*
  * bsa_score_blocks -- the cheap selector (block pooling + scoring).
@@ -414,9 +418,174 @@ bsa_status_t bsa_sparse_attn_decode_noalloc(const bsa_shape_t* shape, const void
                                             const void* v_cache, const int* idx, int idx_stride,
                                             float softmax_scale, void* o, float* lse, void* stream);
 
+/*
+ * Rotation by position, for bsa_qkv_norm_rope.  The first rot_dim channels of
+ * a query or key head are rot_dim/2 pairs; pair i of a token at position t is
+ * turned by the angle t * inv_freq[i] and multiplied by `scale`:
+ *   (a, b) -> scale * (a cos - b sin, a sin + b cos).
+ * Channels from rot_dim on are left as they are.  inv_freq: DEVICE pointer,
+ * rot_dim/2 doubles, 8-byte aligned (NULL, with rot_dim 0, for BSA_ROPE_NONE).
+ */
+typedef struct {
+  int layout;              /* BSA_ROPE_* */
+  int rot_dim;             /* a multiple of 8, at most d */
+  const double* inv_freq;
+  float scale;             /* 1, or the factor of a scaling for long contexts */
+} bsa_rope_t;
+
+/*
+ * bsa_rope_inv_freq -- the frequencies inv_freq[i] = base^(-2i/rot_dim),
+ * i < rot_dim/2, or scaled ones for contexts `factor` times as long as the
+ * original_len tokens of training.  A host function: inv_freq is HOST memory.
+ *   BSA_ROPE_PLAIN   as above; factor and the rest are not read
+ *   BSA_ROPE_LINEAR  every frequency divided by factor
+ *   BSA_ROPE_BASE    base * factor^(rot_dim/(rot_dim-2)): the fastest pair
+ *                    keeps its frequency, the slowest is divided by factor
+ *   BSA_ROPE_PARTS   by the turns r = original_len * f / (2 pi) that a pair
+ *                    makes within original_len: r >= beta_fast keeps f, r <=
+ *                    beta_slow divides it by factor, a ramp linear in r between
+ * *scale (optional) receives 0.1 ln(factor) + 1 for PARTS and 1 otherwise: the
+ * factor on the rotated values that goes with it (set bsa_rope_t.scale to 1
+ * for a model trained without it).
+ */
+bsa_status_t bsa_rope_inv_freq(int rot_dim, double base, int scaling, double factor, double original_len,
+                               double beta_fast, double beta_slow, double* inv_freq, float* scale);
+
+/*
+ * bsa_qkv_norm_rope -- from a fused projection to the attention's inputs in
+ * one pass: per-head RMS norm of queries and keys, rotation by position,
+ * token-major to head-major.  (The pages take Q and K as already encoded;
+ * this is the encoding.)
+ * shape: B, Hq, Hkv, Nq, d, dtype (Nk and block are not read).
+ * qkv: token t of sequence b at qkv + (b*Nq + t)*token_stride elements: its
+ *   Hq query heads, then Hkv key heads, then Hkv value heads, d channels each.
+ *   token_stride >= (Hq + 2 Hkv) d (a slice of a wider projection may be
+ *   passed), its bytes a multiple of 16.
+ * q_weight, k_weight [d] (dtype): y = x / sqrt(mean(x^2) + eps) * weight.
+ *   Both or neither; NULL: no norm.  eps >= 0.
+ * rope: see bsa_rope_t; NULL or BSA_ROPE_NONE: no rotation.
+ * positions [B, Nq] int32 (optional): the tokens' positions, any int32; NULL:
+ *   0..Nq-1.  Angles are formed to 2^-32 turns at any position.
+ * q [B,Hq,Nq,d], k and v [B,Hkv,Nq,d] (dtype) outputs: fp32 inside, rounded
+ *   once.  Outputs must not overlap qkv.
+ * Built: BF16 and F32, d a multiple of 8 and at most 256.
+ */
+bsa_status_t bsa_qkv_norm_rope(const bsa_shape_t* shape, const void* qkv, long long token_stride,
+                               const void* q_weight, const void* k_weight, float eps, const bsa_rope_t* rope,
+                               const int* positions, void* q, void* k, void* v, void* stream);
+
+/*
+ * bsa_qkv_norm_rope_bwd -- the backward of bsa_qkv_norm_rope: from fp32
+ * gradients of q, k, v (as bsa_gated_attn_bwd writes them) to those of qkv and
+ * of the weights.
+ * Inputs: the forward's, and dq [B,Hq,Nq,d], dk and dv [B,Hkv,Nq,d] fp32.
+ * d_qkv: laid out as qkv with d_token_stride; dtype, rounded once; every head's
+ *   channels are written, elements between tokens are left as they are.
+ * d_q_weight, d_k_weight [d] fp32: written (not added to); required with
+ *   weights, NULL without.  Sums run in a fixed order: equal inputs give equal
+ *   bits.
+ * workspace: bsa_workspace_bytes_norm_rope(shape) bytes, 256-byte aligned (NULL
+ *   without weights); its contents on entry do not matter.
+ */
+bsa_status_t bsa_qkv_norm_rope_bwd(const bsa_shape_t* shape, const void* qkv, long long token_stride,
+                                   const void* q_weight, const void* k_weight, float eps, const bsa_rope_t* rope,
+                                   const int* positions, const float* dq, const float* dk, const float* dv,
+                                   void* d_qkv, long long d_token_stride, float* d_q_weight, float* d_k_weight,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scratch bytes of bsa_qkv_norm_rope_bwd; 0 on a bad shape. */
+size_t bsa_workspace_bytes_norm_rope(const bsa_shape_t* shape);
+
+/*
+ * bsa_paged_append_quant -- bsa_paged_append into a cache of 8 bits: new
+ * tokens are quantised as they are written, and every completed block gets its
+ * mean key.
+ * Cite: 稀疏注意力 tutorial §7 (PagedAttention) and §4.6 (one pooled key per
+ * block); Sparse Frontier review §2.4.2 (the retained cache grows).
+ * Format: a row (one token's key or value of one KV head) is d codes e4m3 and
+ *   one exponent byte e; a value is code * 2^(e-127).  e is the least that
+ *   brings the row's largest finite magnitude within 448, kept within
+ *   [10, 246]; codes are rounded to nearest, ties to even (at most 2^-4 of the
+ *   value off; values under 2^(e-133) have steps of 2^(e-136)).  What is stored
+ *   is exact in bf16.  Infinities and NaN are stored as NaN.
+ * k_pool/v_pool [num_pages, Hkv, 64, d] bytes, k_exp/v_exp [num_pages, Hkv, 64]
+ *   bytes: distinct arrays, all 16-byte aligned.
+ * k_new/v_new [B, Hkv, Nq, d] bf16; seq_lens, block_table, table_stride,
+ *   pooled_k as for bsa_paged_append (a completed block's mean is that of the
+ *   stored values).  shape->Nk is not read but for its check.
+ * new_lens [B] int32 (optional): only tokens t < new_lens[b] of sequence b are
+ *   written, of a padded batch (NULL: all Nq; taken within [0, Nq]).
+ * A position past the table or a table entry outside [0, num_pages) is skipped
+ * and flagged (BSA_DEV_BAD_INDEX).  No page may be written by two sequences of
+ * one call.  Built: BF16, block 64, d a multiple of 8 and at most 256.
+ */
+bsa_status_t bsa_paged_append_quant(const bsa_shape_t* shape, const void* k_new, const void* v_new,
+                                    const int* seq_lens, const int* new_lens, const int* block_table,
+                                    int table_stride, int num_pages, void* k_pool, void* v_pool, void* k_exp,
+                                    void* v_exp, float* pooled_k, void* stream);
+
+/*
+ * bsa_paged_read_quant -- tokens of the quantised cache read back as dense
+ * rows, e.g. the keys and values in front of a prefill over a cached context.
+ * Token starts[b] + t of sequence b, t < Nq, becomes row t of k_out/v_out
+ * [B, Hkv, Nq, d] (dtype: BF16, exact, or F32; either may be NULL, not both);
+ * rows at or past the sequence's length seq_lens[b] are left as they were.
+ * starts [B] int32 (optional, NULL: 0), entries >= 0.  Pools, exponents, table
+ * and flags as for bsa_paged_append_quant; outputs 16-byte aligned.
+ */
+bsa_status_t bsa_paged_read_quant(const bsa_shape_t* shape, const void* k_pool, const void* v_pool,
+                                  const void* k_exp, const void* v_exp, int num_pages, const int* block_table,
+                                  int table_stride, const int* seq_lens, const int* starts, void* k_out,
+                                  void* v_out, void* stream);
+
+/*
+ * bsa_sparse_attn_decode_quant -- decode attention over the quantised paged
+ * cache, each sequence its own length.
+ * Cite: 稀疏注意力 tutorial §5 (decode) and §7 (PagedAttention); Sparse
+ * Frontier review §2.4.2 (full cache retained, selective loading).
+ * q [B,Hq,d] bf16; pools, exponents and table as bsa_paged_append_quant keeps
+ *   them, table_stride >= nb = Nk/64.
+ * seq_lens [B] int32 (optional): the tokens sequence b holds, the query's own
+ *   among them if it was appended; taken within [0, Nk].  NULL: Nk each.  What
+ *   lies behind a sequence's last token is neither read from the table nor
+ *   allowed to reach the result.
+ * idx [B,Hkv,idx_stride] int32 LOGICAL block ids, or NULL with idx_stride 0:
+ *   every block of each sequence.  Entries below 0 name no block, wherever
+ *   they stand; a block given twice counts twice; a block past the sequence's
+ *   own length has no keys; an entry >= nb, or a needed table entry outside
+ *   [0, num_pages), is skipped and flagged (BSA_DEV_BAD_INDEX).
+ * o [B,Hq,d] bf16; lse [B,Hq] fp32 (optional), natural log.  A row without a
+ *   key gives o = 0 and lse = -inf.
+ * workspace: bsa_workspace_bytes(BSA_OP_DECODE_QUANT, shape, idx_stride) bytes,
+ *   256-byte aligned; its contents on entry do not matter; calls that may
+ *   overlap need one each.
+ * Built: BF16, d in {64, 128}, block = 64, at most 16 query heads per KV group,
+ *   B <= 8192, num_pages * Hkv < 2^29.
+ */
+bsa_status_t bsa_sparse_attn_decode_quant(const bsa_shape_t* shape, const void* q, const void* k_pool,
+                                          const void* v_pool, const void* k_exp, const void* v_exp, int num_pages,
+                                          const int* block_table, int table_stride, const int* seq_lens,
+                                          const int* idx, int idx_stride, float softmax_scale, void* workspace,
+                                          size_t workspace_bytes, void* o, float* lse, void* stream);
+
+/*
+ * bsa_topk_select_lens -- bsa_topk_select(BSA_TOPK_LAST_BLOCK) for rows whose
+ * sequences have their own lengths.
+ * Cite: SAS page, 推理 paragraph and 核心模块 3; 稀疏注意力 tutorial §5.
+ * scores [rows, ncols] fp32; row r belongs to sequence r / rows_per_len, which
+ * holds lens[r / rows_per_len] tokens = n blocks of `block` (the last may be
+ * partial).  Candidates j < n-1; block n-1 always kept; columns from n-1 on are
+ * not read.  Order and outputs as bsa_topk_select (idx_stride >= kb + 1); a
+ * sequence without tokens keeps nothing.  A length of more than ncols blocks is
+ * taken as ncols blocks and flagged (BSA_DEV_BAD_INDEX).  rows must be a
+ * multiple of rows_per_len.  Limits: ncols <= 8192.
+ */
+bsa_status_t bsa_topk_select_lens(const float* scores, int rows, int ncols, const int* lens, int rows_per_len,
+                                  int block, int kb, int* idx_out, int idx_stride, int* count_out, void* stream);
+
 /* Scratch bytes a decode call needs (op = BSA_OP_*; budget = idx_stride for
- * BSA_OP_DECODE and BSA_OP_DECODE_HEADS, topk for BSA_OP_GIST_DECODE).  0 on
- * a bad shape. */
+ * BSA_OP_DECODE, BSA_OP_DECODE_HEADS and BSA_OP_DECODE_QUANT (there 0 = every
+ * block), topk for BSA_OP_GIST_DECODE).  0 on a bad shape. */
 size_t bsa_workspace_bytes(int op, const bsa_shape_t* shape, int budget);
 
 /* Human-readable name of a status code (static string). */

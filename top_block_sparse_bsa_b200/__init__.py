@@ -29,6 +29,10 @@ __all__ = [
     "bsa_topk_select_joint_heads", "bsa_sparse_attn_decode_heads", "bsa_sparse_attn_decode_paged",
     "bsa_paged_append", "bsa_hssa_decode", "bsa_workspace_bytes_hssa", "bsa_gated_attn_bwd",
     "bsa_workspace_bytes_bwd", "EXPORTED_SYMBOLS",
+    "BSA_OP_DECODE_QUANT", "BSA_ROPE_NONE", "BSA_ROPE_HALF", "BSA_ROPE_PAIRS", "BSA_ROPE_PLAIN", "BSA_ROPE_LINEAR",
+    "BSA_ROPE_BASE", "BSA_ROPE_PARTS", "BsaRope", "make_rope", "bsa_rope_inv_freq", "bsa_qkv_norm_rope",
+    "bsa_qkv_norm_rope_bwd", "bsa_workspace_bytes_norm_rope", "bsa_paged_append_quant", "bsa_paged_read_quant",
+    "bsa_sparse_attn_decode_quant", "bsa_topk_select_lens",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbsa.so")
@@ -37,7 +41,9 @@ BSA_OK, BSA_ERR_INVALID_ARG, BSA_ERR_UNSUPPORTED, BSA_ERR_CUDA, BSA_ERR_TIMEOUT,
 BSA_F32, BSA_BF16 = 0, 1
 BSA_SCORE_PREFILL, BSA_SCORE_DECODE, BSA_SCORE_GIST, BSA_SCORE_DECODE_HEADS = 0, 1, 2, 3
 BSA_TOPK_CAUSAL_BLOCK, BSA_TOPK_LAST_BLOCK, BSA_TOPK_PLAIN = 0, 1, 2
-BSA_OP_DECODE, BSA_OP_GIST_DECODE, BSA_OP_DECODE_HEADS = 0, 1, 2
+BSA_OP_DECODE, BSA_OP_GIST_DECODE, BSA_OP_DECODE_HEADS, BSA_OP_DECODE_QUANT = 0, 1, 2, 3
+BSA_ROPE_NONE, BSA_ROPE_HALF, BSA_ROPE_PAIRS = 0, 1, 2
+BSA_ROPE_PLAIN, BSA_ROPE_LINEAR, BSA_ROPE_BASE, BSA_ROPE_PARTS = 0, 1, 2, 3
 
 # Every symbol the C header declares.
 EXPORTED_SYMBOLS = (
@@ -47,7 +53,9 @@ EXPORTED_SYMBOLS = (
     "bsa_decode_split_override", "bsa_selftest_wait_expiry", "bsa_prefill_kernel_override",
     "bsa_decode_select", "bsa_topk_select_pattern", "bsa_topk_select_joint_heads", "bsa_sparse_attn_decode_heads",
     "bsa_sparse_attn_decode_paged", "bsa_paged_append", "bsa_hssa_decode", "bsa_workspace_bytes_hssa",
-    "bsa_gated_attn_bwd", "bsa_workspace_bytes_bwd",
+    "bsa_gated_attn_bwd", "bsa_workspace_bytes_bwd", "bsa_rope_inv_freq", "bsa_qkv_norm_rope",
+    "bsa_qkv_norm_rope_bwd", "bsa_workspace_bytes_norm_rope", "bsa_paged_append_quant", "bsa_paged_read_quant",
+    "bsa_sparse_attn_decode_quant", "bsa_topk_select_lens",
 )
 
 
@@ -66,8 +74,16 @@ class BsaShape(ctypes.Structure):
                 f"d={self.d}, block={self.block}, dtype={self.dtype})")
 
 
+class BsaRope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
+                ("scale", ctypes.c_float)]
+
+
 _p = ctypes.c_void_p
 _i = ctypes.c_int
+_d = ctypes.c_double
+_ll = ctypes.c_longlong
+_f = ctypes.c_float
 _SIGS = {
     "bsa_score_blocks": (_i, [ctypes.POINTER(BsaShape), _i, _p, _p, _p, _p, _p, _p, _p]),
     "bsa_topk_select": (_i, [_p, _i, _i, _i, _i, _p, _i, _p, _p]),
@@ -100,6 +116,17 @@ _SIGS = {
     "bsa_decode_split_override": (_i, [_i]),
     "bsa_prefill_kernel_override": (_i, [_i]),
     "bsa_selftest_wait_expiry": (_i, [ctypes.c_longlong, _p]),
+    "bsa_rope_inv_freq": (_i, [_i, _d, _i, _d, _d, _d, _d, _p, _p]),
+    "bsa_qkv_norm_rope": (_i, [ctypes.POINTER(BsaShape), _p, _ll, _p, _p, _f, ctypes.POINTER(BsaRope), _p, _p, _p, _p,
+                               _p]),
+    "bsa_qkv_norm_rope_bwd": (_i, [ctypes.POINTER(BsaShape), _p, _ll, _p, _p, _f, ctypes.POINTER(BsaRope), _p, _p, _p,
+                                   _p, _p, _ll, _p, _p, _p, ctypes.c_size_t, _p]),
+    "bsa_workspace_bytes_norm_rope": (ctypes.c_size_t, [ctypes.POINTER(BsaShape)]),
+    "bsa_paged_append_quant": (_i, [ctypes.POINTER(BsaShape), _p, _p, _p, _p, _p, _i, _i, _p, _p, _p, _p, _p, _p]),
+    "bsa_paged_read_quant": (_i, [ctypes.POINTER(BsaShape), _p, _p, _p, _p, _i, _p, _i, _p, _p, _p, _p, _p]),
+    "bsa_sparse_attn_decode_quant": (_i, [ctypes.POINTER(BsaShape), _p, _p, _p, _p, _p, _i, _p, _i, _p, _p, _i, _f, _p,
+                                          ctypes.c_size_t, _p, _p, _p]),
+    "bsa_topk_select_lens": (_i, [_p, _i, _i, _p, _i, _i, _i, _p, _i, _p, _p]),
 }
 
 
@@ -320,3 +347,153 @@ def bsa_sparse_attn_decode_noalloc(shape: BsaShape, q, k_cache, v_cache, idx, id
     _check("bsa_sparse_attn_decode_noalloc", lib.bsa_sparse_attn_decode_noalloc(
         ctypes.byref(shape), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(idx), int(idx_stride),
         ctypes.c_float(softmax_scale), _ptr(o), _ptr(lse), _stream(stream)))
+
+
+def make_rope(layout: int, inv_freq=None, scale: float = 1.0) -> Optional[BsaRope]:
+    """Rotation of the first 2*len(inv_freq) channels (inv_freq: float64 on the device, kept alive by the caller);
+    None for BSA_ROPE_NONE."""
+    if layout == BSA_ROPE_NONE:
+        if inv_freq is not None:
+            raise ValueError("BSA_ROPE_NONE takes no frequencies")
+        return None
+    if inv_freq is None:
+        raise ValueError("a rotation needs its frequencies")
+    if inv_freq.dtype != torch.float64:
+        raise ValueError(f"inv_freq is float64, got {inv_freq.dtype}")
+    return BsaRope(int(layout), 2 * inv_freq.numel(), _ptr(inv_freq), float(scale))
+
+
+def bsa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: int = BSA_ROPE_PLAIN, factor: float = 1.0,
+                      original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(frequencies [rot_dim/2] float64 on the host, factor on the rotated values)."""
+    out = torch.empty((max(int(rot_dim), 0) // 2,), dtype=torch.float64)
+    scale = ctypes.c_float(0.0)
+    _check("bsa_rope_inv_freq", lib.bsa_rope_inv_freq(
+        int(rot_dim), float(base), int(scaling), float(factor), float(original_len), float(beta_fast),
+        float(beta_slow), ctypes.c_void_p(out.data_ptr() if out.numel() else None), ctypes.byref(scale)))
+    return out, float(scale.value)
+
+
+def _same_type(what: str, dtype: torch.dtype, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{what} takes {dtype}, got {t.dtype}")
+
+
+def _one_device(*tensors) -> None:
+    """The calls run on the current device and its current stream: their tensors live there."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"a tensor on {t.device} in a call on cuda:{here}")
+
+
+def _token_rows(what: str, x, heads: int, d: int):
+    """Pointer and token stride of x [B, N, heads, d]: dense but for the distance between tokens."""
+    if not x.is_cuda:
+        raise ValueError("libbsa takes device tensors")
+    B, N = x.shape[:2]
+    token = x.stride(1) if N > 1 else (x.stride(0) if B > 1 else heads * d)
+    if x.shape[2:] != (heads, d) or (d > 1 and x.stride(3) != 1) or (heads > 1 and x.stride(2) != d) or \
+            (B > 1 and x.stride(0) != N * token):
+        raise ValueError(f"{what}: [B, N, {heads}, {d}] rows, tokens evenly apart")
+    return ctypes.c_void_p(x.data_ptr()), token
+
+
+def _size(t) -> ctypes.c_size_t:
+    return ctypes.c_size_t(t.numel() * t.element_size() if t is not None else 0)
+
+
+def bsa_workspace_bytes_norm_rope(shape: BsaShape) -> int:
+    return int(lib.bsa_workspace_bytes_norm_rope(ctypes.byref(shape)))
+
+
+def bsa_qkv_norm_rope(shape: BsaShape, qkv, q_weight, k_weight, eps: float, rope: Optional[BsaRope], positions,
+                      q, k, v, stream=None) -> None:
+    """Norms, rotation and change to head-major of qkv [B, Nq, Hq+2Hkv, d] (a slice of wider rows may be given)."""
+    _same_type("bsa_qkv_norm_rope", qkv.dtype, q_weight, k_weight, q, k, v)
+    _one_device(qkv, q_weight, k_weight, positions, q, k, v)
+    if positions is not None:
+        _same_type("positions", torch.int32, positions)
+    src, token_stride = _token_rows("qkv", qkv, shape.Hq + 2 * shape.Hkv, shape.d)
+    _check("bsa_qkv_norm_rope", lib.bsa_qkv_norm_rope(
+        ctypes.byref(shape), src, token_stride, _ptr(q_weight), _ptr(k_weight), eps,
+        ctypes.byref(rope) if rope is not None else None, _ptr(positions), _ptr(q), _ptr(k), _ptr(v), _stream(stream)))
+
+
+def bsa_qkv_norm_rope_bwd(shape: BsaShape, qkv, q_weight, k_weight, eps: float, rope: Optional[BsaRope], positions,
+                          dq, dk, dv, d_qkv, d_q_weight=None, d_k_weight=None, workspace=None, stream=None) -> None:
+    """Gradients of qkv and of the norms' weights from fp32 dq, dk, dv."""
+    _same_type("bsa_qkv_norm_rope_bwd", qkv.dtype, q_weight, k_weight, d_qkv)
+    _same_type("the gradients of bsa_qkv_norm_rope_bwd", torch.float32, dq, dk, dv, d_q_weight, d_k_weight)
+    _one_device(qkv, q_weight, k_weight, positions, dq, dk, dv, d_qkv, d_q_weight, d_k_weight, workspace)
+    if positions is not None:
+        _same_type("positions", torch.int32, positions)
+    heads = shape.Hq + 2 * shape.Hkv
+    src, token_stride = _token_rows("qkv", qkv, heads, shape.d)
+    dst, d_token_stride = _token_rows("d_qkv", d_qkv, heads, shape.d)
+    _check("bsa_qkv_norm_rope_bwd", lib.bsa_qkv_norm_rope_bwd(
+        ctypes.byref(shape), src, token_stride, _ptr(q_weight), _ptr(k_weight), eps,
+        ctypes.byref(rope) if rope is not None else None, _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dv), dst,
+        d_token_stride, _ptr(d_q_weight), _ptr(d_k_weight), _ptr(workspace), _size(workspace), _stream(stream)))
+
+
+def _quant_pools(what: str, k_pool, v_pool, k_exp, v_exp) -> None:
+    for t in (k_pool, v_pool):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError(f"{what}: pools hold e4m3 codes (float8_e4m3fn or uint8), got {t.dtype}")
+    _same_type(what + ": exponents", torch.uint8, k_exp, v_exp)
+    if k_pool.shape != v_pool.shape or k_exp.shape != k_pool.shape[:3] or v_exp.shape != k_exp.shape:
+        raise ValueError(f"{what}: pools [P,Hkv,64,d] and exponents [P,Hkv,64] do not match")
+    _one_device(k_pool, v_pool, k_exp, v_exp)
+
+
+def bsa_paged_append_quant(shape: BsaShape, k_new, v_new, seq_lens, block_table, k_pool, v_pool, k_exp, v_exp,
+                           pooled_k=None, new_lens=None, stream=None) -> None:
+    """Quantise k_new/v_new [B,Hkv,T,d] into positions seq_lens[b]+t (t < new_lens[b]) of the paged cache; pool
+    completed blocks."""
+    _quant_pools("bsa_paged_append_quant", k_pool, v_pool, k_exp, v_exp)
+    _same_type("bsa_paged_append_quant", torch.bfloat16, k_new, v_new)
+    _same_type("lengths and table", torch.int32, seq_lens, new_lens, block_table)
+    _one_device(k_new, v_new, seq_lens, new_lens, block_table, pooled_k)
+    _check("bsa_paged_append_quant", lib.bsa_paged_append_quant(
+        ctypes.byref(shape), _ptr(k_new), _ptr(v_new), _ptr(seq_lens), _ptr(new_lens), _ptr(block_table),
+        int(block_table.shape[-1]), int(k_pool.shape[0]), _ptr(k_pool), _ptr(v_pool), _ptr(k_exp), _ptr(v_exp),
+        _ptr(pooled_k), _stream(stream)))
+
+
+def bsa_paged_read_quant(shape: BsaShape, k_pool, v_pool, k_exp, v_exp, block_table, seq_lens, k_out, v_out,
+                         starts=None, stream=None) -> None:
+    """Tokens starts[b]+t of the quantised cache as dense rows [B,Hkv,T,d]; rows past a sequence stay as they were."""
+    _quant_pools("bsa_paged_read_quant", k_pool, v_pool, k_exp, v_exp)
+    _same_type("lengths and table", torch.int32, seq_lens, starts, block_table)
+    _same_type("bsa_paged_read_quant", torch.bfloat16 if shape.dtype == BSA_BF16 else torch.float32, k_out, v_out)
+    _one_device(block_table, seq_lens, starts, k_out, v_out)
+    _check("bsa_paged_read_quant", lib.bsa_paged_read_quant(
+        ctypes.byref(shape), _ptr(k_pool), _ptr(v_pool), _ptr(k_exp), _ptr(v_exp), int(k_pool.shape[0]),
+        _ptr(block_table), int(block_table.shape[-1]), _ptr(seq_lens), _ptr(starts), _ptr(k_out), _ptr(v_out),
+        _stream(stream)))
+
+
+def bsa_sparse_attn_decode_quant(shape: BsaShape, q, k_pool, v_pool, k_exp, v_exp, block_table, seq_lens, idx,
+                                 idx_stride: int, softmax_scale: float, workspace, o, lse=None, stream=None) -> None:
+    """Decode over the quantised paged cache: kept blocks idx [B,Hkv,idx_stride], or every block (None, 0)."""
+    _quant_pools("bsa_sparse_attn_decode_quant", k_pool, v_pool, k_exp, v_exp)
+    _same_type("bsa_sparse_attn_decode_quant", torch.bfloat16, q, o)
+    _same_type("lengths, lists and table", torch.int32, seq_lens, idx, block_table)
+    _one_device(q, block_table, seq_lens, idx, workspace, o, lse)
+    _check("bsa_sparse_attn_decode_quant", lib.bsa_sparse_attn_decode_quant(
+        ctypes.byref(shape), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_exp), _ptr(v_exp), int(k_pool.shape[0]),
+        _ptr(block_table), int(block_table.shape[-1]), _ptr(seq_lens), _ptr(idx), int(idx_stride), softmax_scale,
+        _ptr(workspace), _size(workspace), _ptr(o), _ptr(lse), _stream(stream)))
+
+
+def bsa_topk_select_lens(scores, rows: int, ncols: int, lens, rows_per_len: int, block: int, kb: int, idx_out,
+                         idx_stride: int, count_out=None, stream=None) -> None:
+    """Decode selection where row r's sequence r // rows_per_len holds lens[r // rows_per_len] tokens."""
+    _same_type("scores", torch.float32, scores)
+    _same_type("lengths and lists", torch.int32, lens, idx_out, count_out)
+    _one_device(scores, lens, idx_out, count_out)
+    _check("bsa_topk_select_lens", lib.bsa_topk_select_lens(
+        _ptr(scores), int(rows), int(ncols), _ptr(lens), int(rows_per_len), int(block), int(kb), _ptr(idx_out),
+        int(idx_stride), _ptr(count_out), _stream(stream)))

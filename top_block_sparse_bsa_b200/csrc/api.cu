@@ -240,6 +240,26 @@ HssaLayout hssa_layout(const bsa_shape_t* s, int km, int topk, int num_sms) {
   return L;
 }
 
+// Workspace of the decode over the quantised cache: the sequences' first list
+// positions, then two partial records per block of threads and head.
+struct QuantLayout {
+  size_t pre, partial, total;
+  int num_ctas;
+};
+
+QuantLayout quant_layout(const bsa_shape_t* s, int num_sms) {
+  QuantLayout L{};
+  const int forced = g_split_override.load(std::memory_order_relaxed);
+  L.num_ctas = forced > 0 ? forced : quant_decode_ctas(num_sms);
+  size_t off = 0;
+  L.pre = off;
+  off = align256(off + (static_cast<size_t>(s->B) + 1) * sizeof(int));
+  L.partial = off;
+  off = align256(off + static_cast<size_t>(L.num_ctas) * 2 * (s->Hq / s->Hkv) * (s->d + 4) * sizeof(float));
+  L.total = off;
+  return L;
+}
+
 // Self-test of the bounded-wait expiry path: one thread waits, with a small
 // budget, on a shared-memory barrier that nothing arrives on.  The wait gives
 // up, raises BSA_DEV_TIMEOUT in the status word and the kernel returns.
@@ -340,6 +360,7 @@ size_t bsa_workspace_bytes(int op, const bsa_shape_t* s, int budget) {
     if (budget < 1) return 0;
     return heads_layout(s, budget, sms).total;
   }
+  if (op == BSA_OP_DECODE_QUANT) return quant_layout(s, sms).total;
   return 0;
 }
 
@@ -794,6 +815,260 @@ bsa_status_t bsa_paged_append(const bsa_shape_t* s, const void* k_new, const voi
   return cuda_status(launch_paged_append(k_new, v_new, s->B, s->Hkv, s->Nq, s->d, seq_lens, block_table,
                                          table_stride, num_pages, k_pool, v_pool, pooled_k, status,
                                          static_cast<cudaStream_t>(stream)));
+}
+
+bsa_status_t bsa_rope_inv_freq(int rot_dim, double base, int scaling, double factor, double original_len,
+                               double beta_fast, double beta_slow, double* inv_freq, float* scale) {
+  if (inv_freq == nullptr || rot_dim < 2 || rot_dim % 2 != 0 || !(base > 0.0) || !isfinite(base))
+    return BSA_ERR_INVALID_ARG;
+  if (scaling < BSA_ROPE_PLAIN || scaling > BSA_ROPE_PARTS) return BSA_ERR_INVALID_ARG;
+  if (scaling != BSA_ROPE_PLAIN && !(factor >= 1.0 && isfinite(factor))) return BSA_ERR_INVALID_ARG;
+  if (scaling == BSA_ROPE_PARTS && !(original_len > 0.0 && isfinite(original_len) && beta_slow > 0.0 &&
+                                     beta_fast > beta_slow && isfinite(beta_fast)))
+    return BSA_ERR_INVALID_ARG;
+  if (scaling == BSA_ROPE_BASE && rot_dim > 2) base *= pow(factor, rot_dim / (rot_dim - 2.0));
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot_dim);
+    if (scaling == BSA_ROPE_LINEAR) f /= factor;
+    if (scaling == BSA_ROPE_PARTS) {
+      const double turns = original_len * f / 6.283185307179586476925;
+      const double keep = std::min(1.0, std::max(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    inv_freq[i] = f;
+  }
+  if (scale) *scale = scaling == BSA_ROPE_PARTS ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
+  return BSA_OK;
+}
+
+// Checks shared by the norm + rotation calls; fills the arguments they share.
+static bsa_status_t norm_rope_checks(const bsa_shape_t* s, const void* qkv, long long token_stride,
+                                     const void* q_weight, const void* k_weight, float eps, const bsa_rope_t* rope,
+                                     const int* positions, NormRopeArgs* a) {
+  if (s == nullptr || qkv == nullptr) return BSA_ERR_INVALID_ARG;
+  if (s->B <= 0 || s->Hq <= 0 || s->Hkv <= 0 || s->Nq <= 0 || s->d <= 0) return BSA_ERR_INVALID_ARG;
+  if (s->dtype != BSA_F32 && s->dtype != BSA_BF16) return BSA_ERR_INVALID_ARG;
+  if ((q_weight == nullptr) != (k_weight == nullptr) || !(eps >= 0.0f)) return BSA_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(q_weight) || !aligned16(k_weight)) return BSA_ERR_INVALID_ARG;
+  const int size = s->dtype == BSA_BF16 ? 2 : 4;
+  const int64_t heads = static_cast<int64_t>(s->Hq) + 2 * static_cast<int64_t>(s->Hkv);
+  if (token_stride < heads * s->d || token_stride * size % 16 != 0) return BSA_ERR_INVALID_ARG;
+  const int layout = rope ? rope->layout : BSA_ROPE_NONE;
+  if (layout != BSA_ROPE_NONE) {
+    if (layout != BSA_ROPE_HALF && layout != BSA_ROPE_PAIRS) return BSA_ERR_INVALID_ARG;
+    if (rope->inv_freq == nullptr || (reinterpret_cast<uintptr_t>(rope->inv_freq) & 7u) != 0 || rope->rot_dim < 1 ||
+        rope->rot_dim > s->d)
+      return BSA_ERR_INVALID_ARG;
+    if (rope->rot_dim % 8 != 0) return BSA_ERR_UNSUPPORTED;
+  }
+  if (s->d % 8 != 0 || s->d > 256 || heads > 65535) return BSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->B) * s->Nq >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
+  a->B = s->B;
+  a->N = s->Nq;
+  a->Hq = s->Hq;
+  a->Hkv = s->Hkv;
+  a->d = s->d;
+  a->layout = layout;
+  a->rot = layout == BSA_ROPE_NONE ? 0 : rope->rot_dim;
+  a->inv_freq = layout == BSA_ROPE_NONE ? nullptr : rope->inv_freq;
+  a->rope_scale = layout == BSA_ROPE_NONE ? 1.0f : rope->scale;
+  a->eps = eps;
+  a->inv_d = static_cast<float>(1.0 / s->d);
+  a->positions = positions;
+  a->qkv = qkv;
+  a->q_weight = q_weight;
+  a->k_weight = k_weight;
+  a->token_stride = token_stride;
+  return BSA_OK;
+}
+
+bsa_status_t bsa_qkv_norm_rope(const bsa_shape_t* s, const void* qkv, long long token_stride, const void* q_weight,
+                               const void* k_weight, float eps, const bsa_rope_t* rope, const int* positions, void* q,
+                               void* k, void* v, void* stream) {
+  NormRopeArgs a{};
+  bsa_status_t st = norm_rope_checks(s, qkv, token_stride, q_weight, k_weight, eps, rope, positions, &a);
+  if (st != BSA_OK) return st;
+  if (!q || !k || !v || !aligned16(q) || !aligned16(k) || !aligned16(v)) return BSA_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  int sms = 0;
+  if ((st = device_state(nullptr, &sms)) != BSA_OK) return st;
+  return cuda_status(launch_norm_rope(a, s->dtype == BSA_BF16, false, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t bsa_workspace_bytes_norm_rope(const bsa_shape_t* s) {
+  if (s == nullptr || s->B <= 0 || s->Nq <= 0 || s->d <= 0 || s->d > 256) return 0;
+  int sms = 0;
+  if (device_state(nullptr, &sms) != BSA_OK) return 0;
+  return align256(static_cast<size_t>(norm_rope_bwd_blocks(sms)) * 2 * s->d * sizeof(float));
+}
+
+bsa_status_t bsa_qkv_norm_rope_bwd(const bsa_shape_t* s, const void* qkv, long long token_stride,
+                                   const void* q_weight, const void* k_weight, float eps, const bsa_rope_t* rope,
+                                   const int* positions, const float* dq, const float* dk, const float* dv,
+                                   void* d_qkv, long long d_token_stride, float* d_q_weight, float* d_k_weight,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  NormRopeArgs a{};
+  bsa_status_t st = norm_rope_checks(s, qkv, token_stride, q_weight, k_weight, eps, rope, positions, &a);
+  if (st != BSA_OK) return st;
+  if (!dq || !dk || !dv || !d_qkv) return BSA_ERR_INVALID_ARG;
+  if (!aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(d_qkv)) return BSA_ERR_INVALID_ARG;
+  const int size = s->dtype == BSA_BF16 ? 2 : 4;
+  if (d_token_stride < (static_cast<int64_t>(s->Hq) + 2 * static_cast<int64_t>(s->Hkv)) * s->d ||
+      d_token_stride * size % 16 != 0)
+    return BSA_ERR_INVALID_ARG;
+  int sms = 0;
+  if (q_weight != nullptr) {
+    if (!d_q_weight || !d_k_weight || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return BSA_ERR_INVALID_ARG;
+    if ((st = device_state(nullptr, &sms)) != BSA_OK) return st;
+    if (workspace_bytes < bsa_workspace_bytes_norm_rope(s)) return BSA_ERR_INVALID_ARG;
+  } else {
+    if (d_q_weight || d_k_weight) return BSA_ERR_INVALID_ARG;
+    if ((st = device_state(nullptr, &sms)) != BSA_OK) return st;
+  }
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.d_qkv = d_qkv;
+  a.d_token_stride = d_token_stride;
+  a.dw_partial = static_cast<float*>(workspace);
+  a.d_q_weight = d_q_weight;
+  a.d_k_weight = d_k_weight;
+  return cuda_status(launch_norm_rope(a, s->dtype == BSA_BF16, true, sms, static_cast<cudaStream_t>(stream)));
+}
+
+// Checks shared by the quantised cache's calls.
+static bsa_status_t quant_cache_checks(const bsa_shape_t* s, const void* k_pool, const void* v_pool,
+                                       const void* k_exp, const void* v_exp, int num_pages, const int* block_table,
+                                       int table_stride) {
+  bsa_status_t st = check_shape(s);
+  if (st != BSA_OK) return st;
+  if (!k_pool || !v_pool || !k_exp || !v_exp || !block_table || table_stride < 1 || num_pages < 1)
+    return BSA_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_exp) || !aligned16(v_exp)) return BSA_ERR_INVALID_ARG;
+  if (s->block != 64 || s->d % 8 != 0 || s->d > 256) return BSA_ERR_UNSUPPORTED;
+  // 16-row pieces of the pools are counted in 32 bits
+  if (static_cast<int64_t>(num_pages) * s->Hkv >= (1ll << 29)) return BSA_ERR_UNSUPPORTED;
+  return BSA_OK;
+}
+
+bsa_status_t bsa_paged_append_quant(const bsa_shape_t* s, const void* k_new, const void* v_new, const int* seq_lens,
+                                    const int* new_lens, const int* block_table, int table_stride, int num_pages,
+                                    void* k_pool, void* v_pool, void* k_exp, void* v_exp, float* pooled_k,
+                                    void* stream) {
+  bsa_status_t st = quant_cache_checks(s, k_pool, v_pool, k_exp, v_exp, num_pages, block_table, table_stride);
+  if (st != BSA_OK) return st;
+  if (!k_new || !v_new || !seq_lens || !aligned16(k_new) || !aligned16(v_new)) return BSA_ERR_INVALID_ARG;
+  if (k_pool == v_pool || k_exp == v_exp || (pooled_k && !aligned16(pooled_k))) return BSA_ERR_INVALID_ARG;
+  if (s->dtype != BSA_BF16) return BSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->B) * s->Hkv * ((s->Nq + 62) / 64 + 1) >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
+  QuantCacheArgs a{};
+  if ((st = device_state(&a.status, nullptr)) != BSA_OK) return st;
+  a.B = s->B;
+  a.Hkv = s->Hkv;
+  a.T = s->Nq;
+  a.d = s->d;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.num_pages = num_pages;
+  a.k_pool = static_cast<uint8_t*>(k_pool);
+  a.v_pool = static_cast<uint8_t*>(v_pool);
+  a.k_exp = static_cast<uint8_t*>(k_exp);
+  a.v_exp = static_cast<uint8_t*>(v_exp);
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.pooled = pooled_k;
+  return cuda_status(launch_quant_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+bsa_status_t bsa_paged_read_quant(const bsa_shape_t* s, const void* k_pool, const void* v_pool, const void* k_exp,
+                                  const void* v_exp, int num_pages, const int* block_table, int table_stride,
+                                  const int* seq_lens, const int* starts, void* k_out, void* v_out, void* stream) {
+  bsa_status_t st = quant_cache_checks(s, k_pool, v_pool, k_exp, v_exp, num_pages, block_table, table_stride);
+  if (st != BSA_OK) return st;
+  if (!seq_lens || (!k_out && !v_out) || !aligned16(k_out) || !aligned16(v_out)) return BSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(s->B) * s->Hkv * s->Nq * (s->d / 8) >= (1ll << 38)) return BSA_ERR_UNSUPPORTED;
+  QuantCacheArgs a{};
+  if ((st = device_state(&a.status, nullptr)) != BSA_OK) return st;
+  a.B = s->B;
+  a.Hkv = s->Hkv;
+  a.T = s->Nq;
+  a.d = s->d;
+  a.seq_lens = seq_lens;
+  a.starts = starts;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.num_pages = num_pages;
+  a.k_pool = static_cast<uint8_t*>(const_cast<void*>(k_pool));
+  a.v_pool = static_cast<uint8_t*>(const_cast<void*>(v_pool));
+  a.k_exp = static_cast<uint8_t*>(const_cast<void*>(k_exp));
+  a.v_exp = static_cast<uint8_t*>(const_cast<void*>(v_exp));
+  a.k_out = k_out;
+  a.v_out = v_out;
+  return cuda_status(launch_quant_read(a, s->dtype == BSA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+bsa_status_t bsa_sparse_attn_decode_quant(const bsa_shape_t* s, const void* q, const void* k_pool, const void* v_pool,
+                                          const void* k_exp, const void* v_exp, int num_pages, const int* block_table,
+                                          int table_stride, const int* seq_lens, const int* idx, int idx_stride,
+                                          float softmax_scale, void* workspace, size_t workspace_bytes, void* o,
+                                          float* lse, void* stream) {
+  bsa_status_t st = quant_cache_checks(s, k_pool, v_pool, k_exp, v_exp, num_pages, block_table, table_stride);
+  if (st != BSA_OK) return st;
+  if (s->Nq != 1 || !q || !o || !aligned16(q) || !aligned16(o)) return BSA_ERR_INVALID_ARG;
+  const int nb = s->Nk / s->block;
+  if (table_stride < nb || (idx ? idx_stride < 1 : idx_stride != 0)) return BSA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !isfinite(softmax_scale) || !workspace) return BSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return BSA_ERR_INVALID_ARG;
+  if (s->dtype != BSA_BF16 || (s->d != 64 && s->d != 128) || s->Hq / s->Hkv > 16 || s->B > 8192)
+    return BSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->B) * (idx ? idx_stride : nb) >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
+  QuantDecodeArgs a{};
+  int sms = 0;
+  if ((st = device_state(&a.status, &sms)) != BSA_OK) return st;
+  const QuantLayout L = quant_layout(s, sms);
+  if (workspace_bytes < L.total) return BSA_ERR_INVALID_ARG;
+  a.B = s->B;
+  a.Hq = s->Hq;
+  a.Hkv = s->Hkv;
+  a.nb = nb;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_pool = static_cast<const uint8_t*>(k_pool);
+  a.v_pool = static_cast<const uint8_t*>(v_pool);
+  a.k_exp = static_cast<const uint8_t*>(k_exp);
+  a.v_exp = static_cast<const uint8_t*>(v_exp);
+  a.num_pages = num_pages;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.lens = seq_lens;
+  a.idx = idx;
+  a.list_len = idx_stride;
+  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  a.num_ctas = L.num_ctas;
+  a.pre = reinterpret_cast<int*>(static_cast<char*>(workspace) + L.pre);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.partial);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  return cuda_status(launch_attn_decode_quant(a, s->d, static_cast<cudaStream_t>(stream)));
+}
+
+bsa_status_t bsa_topk_select_lens(const float* scores, int rows, int ncols, const int* lens, int rows_per_len,
+                                  int block, int kb, int* idx_out, int idx_stride, int* count_out, void* stream) {
+  if (scores == nullptr || idx_out == nullptr || lens == nullptr || rows < 0 || ncols < 1 || kb < 0 || block < 1)
+    return BSA_ERR_INVALID_ARG;
+  if (rows_per_len < 1 || rows % rows_per_len != 0) return BSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(idx_stride) < static_cast<int64_t>(kb) + 1) return BSA_ERR_INVALID_ARG;
+  if (ncols > 8192) return BSA_ERR_UNSUPPORTED;
+  if (rows == 0) return BSA_OK;
+  uint32_t* status = nullptr;
+  bsa_status_t st = device_state(&status, nullptr);
+  if (st != BSA_OK) return st;
+  return cuda_status(launch_topk_lens(scores, rows, ncols, lens, rows_per_len, block, kb, idx_out, idx_stride,
+                                      count_out, status, static_cast<cudaStream_t>(stream)));
 }
 
 bsa_status_t bsa_hssa_decode(const bsa_shape_t* s, const void* q, const void* k_cache, const void* v_cache,

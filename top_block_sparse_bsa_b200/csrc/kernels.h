@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -133,6 +134,70 @@ cudaError_t launch_attn_bwd(const CUtensorMap* tmQ, const CUtensorMap* tmDO, con
 cudaError_t launch_paged_append(const void* k_new, const void* v_new, int B, int Hkv, int T, int d,
                                 const int* seq_lens, const int* table, int table_stride, int num_pages, void* k_pool,
                                 void* v_pool, float* pooled_k, uint32_t* status, cudaStream_t st);
+
+// norm_rope.cu (query/key norms with the rotation, and their backward)
+struct NormRopeArgs {
+  int B, N, Hq, Hkv, d;
+  int layout, rot;             // BSA_ROPE_*; rotated channels
+  const double* inv_freq;      // [rot/2]
+  float rope_scale, eps, inv_d;
+  const int* positions;        // [B][N] or null (0, 1, ...)
+  const void *qkv, *q_weight, *k_weight;
+  int64_t token_stride;        // elements between tokens of qkv
+  void *q, *k, *v;             // forward: [B][H][N][d]
+  const float *dq, *dk, *dv;   // backward
+  void* d_qkv;
+  int64_t d_token_stride;
+  float *dw_partial, *d_q_weight, *d_k_weight;
+  int head_run;                // set by the launcher: heads per work item
+};
+int norm_rope_bwd_blocks(int num_sms);   // largest grid of the backward = partial records of the weights' gradients
+cudaError_t launch_norm_rope(const NormRopeArgs& a, bool bf16, bool bwd, int num_sms, cudaStream_t st);
+
+// quant_cache.cu (paged cache of e4m3 codes with an exponent byte per row)
+struct QuantCacheArgs {
+  int B, Hkv, T, d;
+  const int* seq_lens;
+  const int* new_lens;         // append: tokens of each sequence (null: T)
+  const int* starts;           // read: first token of each sequence (null: 0)
+  const int* table;
+  int table_stride, num_pages;
+  uint8_t *k_pool, *v_pool, *k_exp, *v_exp;
+  const void *k_new, *v_new;
+  float* pooled;
+  void *k_out, *v_out;
+  uint32_t* status;
+  int touched;                 // set by the launchers
+  int64_t total;
+};
+cudaError_t launch_quant_append(QuantCacheArgs a, cudaStream_t st);
+cudaError_t launch_quant_read(QuantCacheArgs a, bool bf16, cudaStream_t st);
+
+// attn_decode_quant.cu (decode over the quantised paged cache)
+struct QuantDecodeArgs {
+  int B, Hq, Hkv, nb;
+  const __nv_bfloat16* q;
+  const uint8_t *k_pool, *v_pool, *k_exp, *v_exp;
+  int num_pages;
+  const int* table;
+  int table_stride;
+  const int* lens;             // [B] or null (nb * 64)
+  const int* idx;              // [B*Hkv][list_len] or null (every block)
+  int list_len;
+  float scale_log2;
+  int num_ctas;
+  int* pre;                    // workspace: [B+1]
+  float* partial;              // workspace: [num_ctas][2][G][d+4]
+  __nv_bfloat16* o;
+  float* lse;
+  uint32_t* status;
+};
+int quant_decode_ctas(int num_sms);
+cudaError_t launch_attn_decode_quant(const QuantDecodeArgs& a, int d, cudaStream_t st);
+
+// topk_lens.cu
+cudaError_t launch_topk_lens(const float* scores, int rows, int ncols, const int* lens, int rows_per_len, int block,
+                             int kb, int* idx_out, int idx_stride, int* count_out, uint32_t* status, cudaStream_t st);
 
 // attn_f32.cu (fp32 SIMT path)
 cudaError_t launch_attn_prefill_f32(const float* q, const float* k, const float* v, const PrefillArgs& a,

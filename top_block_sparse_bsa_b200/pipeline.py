@@ -19,7 +19,9 @@ from . import (bsa_gated_attn_bwd, bsa_workspace_bytes_bwd, BSA_OP_DECODE, BSA_O
                bsa_gated_attn_fwd, bsa_gist_expand_decode, bsa_score_blocks, bsa_sparse_attn_decode,
                bsa_hssa_decode, bsa_paged_append, bsa_sparse_attn_decode_heads, bsa_workspace_bytes_hssa, bsa_sparse_attn_decode_paged, bsa_sparse_attn_prefill,
                bsa_topk_select, bsa_topk_select_joint_heads, bsa_topk_select_pattern, bsa_workspace_bytes,
-               make_shape)
+               make_shape, BSA_OP_DECODE_QUANT, BSA_ROPE_HALF, BSA_ROPE_NONE, bsa_paged_append_quant,
+               bsa_paged_read_quant, bsa_qkv_norm_rope, bsa_qkv_norm_rope_bwd, bsa_sparse_attn_decode_quant,
+               bsa_topk_select_lens, bsa_workspace_bytes_norm_rope, make_rope)
 
 
 def _dev(t: torch.Tensor):
@@ -376,3 +378,153 @@ class HssaStep:
                         self.meta_v, self.km, self.topk, b["meta_idx"], b["idx"] if self.topk > 0 else None,
                         self.softmax_scale, b["workspace"], b["o"], b["lse"] if with_lse else None, stream=stream)
         return b
+
+
+@dataclass
+class QkvStep:
+    """From a fused projection qkv [B,N,Hq+2Hkv,d] to q [B,Hq,N,d], k and v [B,Hkv,N,d] for the steps here: RMS
+    norm of every query and key head (q_weight and k_weight [d], or None), rotation by position, head-major order.
+
+    inv_freq: float64 [rot_dim/2] on the device (bsa_rope_inv_freq; None: no rotation); positions [B,N] int32 or
+    None (0..N-1); rope_scale: the factor of a scaling for long contexts.  For decode (N = 1), q is
+    bufs["q"][:, :, 0] and k, v are PagedDecodeStep.append's or QuantDecodeStep.append's k_new, v_new."""
+    qkv: torch.Tensor
+    Hq: int
+    Hkv: int
+    q_weight: Optional[torch.Tensor] = None
+    k_weight: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    inv_freq: Optional[torch.Tensor] = None
+    layout: int = BSA_ROPE_HALF
+    positions: Optional[torch.Tensor] = None
+    rope_scale: float = 1.0
+    bufs: Dict[str, torch.Tensor] = field(default_factory=dict)
+
+    def __post_init__(self):
+        B, N, H, d = self.qkv.shape
+        if H != self.Hq + 2 * self.Hkv:
+            raise ValueError(f"qkv has {H} heads a token, not {self.Hq} + 2 * {self.Hkv}")
+        if self.positions is not None and self.positions.shape != (B, N):
+            raise ValueError(f"positions are [{B}, {N}], got {list(self.positions.shape)}")
+        for w in (self.q_weight, self.k_weight):
+            if w is not None and w.shape != (d,):
+                raise ValueError(f"a norm's weight is [{d}], got {list(w.shape)}")
+        self.shape = make_shape(B, self.Hq, self.Hkv, N, N, d, 1, self.qkv.dtype)
+        self.rope = make_rope(self.layout if self.inv_freq is not None else BSA_ROPE_NONE, self.inv_freq,
+                              self.rope_scale)
+        b = self.bufs
+        for name, heads in (("q", self.Hq), ("k", self.Hkv), ("v", self.Hkv)):
+            b.setdefault(name, torch.empty((B, heads, N, d), dtype=self.qkv.dtype, device=self.qkv.device))
+
+    def run(self, stream=None):
+        b = self.bufs
+        bsa_qkv_norm_rope(self.shape, self.qkv, self.q_weight, self.k_weight, self.eps, self.rope, self.positions,
+                          b["q"], b["k"], b["v"], stream=stream)
+        return b
+
+    def backward(self, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, stream=None):
+        """Gradients d_qkv (qkv's type, dense) and, with weights, d_q_weight and d_k_weight (fp32) from fp32 dq, dk,
+        dv, as PrefillStep.backward gives them."""
+        B, N, H, d = self.qkv.shape
+        for name, g, heads in (("dq", dq, self.Hq), ("dk", dk, self.Hkv), ("dv", dv, self.Hkv)):
+            if g.shape != (B, heads, N, d):
+                raise ValueError(f"{name} is [{B}, {heads}, {N}, {d}], got {list(g.shape)}")
+        b = self.bufs
+        dev = self.qkv.device
+        if "d_qkv" not in b:
+            b["d_qkv"] = torch.empty((B, N, H, d), dtype=self.qkv.dtype, device=dev)
+        if self.q_weight is not None and "d_q_weight" not in b:
+            b["d_q_weight"] = torch.empty((d,), dtype=torch.float32, device=dev)
+            b["d_k_weight"] = torch.empty((d,), dtype=torch.float32, device=dev)
+            b["qkv_workspace"] = torch.empty((bsa_workspace_bytes_norm_rope(self.shape),), dtype=torch.uint8,
+                                             device=dev)
+        bsa_qkv_norm_rope_bwd(self.shape, self.qkv, self.q_weight, self.k_weight, self.eps, self.rope, self.positions,
+                              dq, dk, dv, b["d_qkv"], b.get("d_q_weight"), b.get("d_k_weight"),
+                              b.get("qkv_workspace"), stream=stream)
+        return b
+
+
+@dataclass
+class QuantDecodeStep:
+    """Decode over a paged KV cache of 8 bits whose sequences have their own lengths: pools [P,Hkv,64,d] of e4m3
+    codes, exponents [P,Hkv,64], a block table [B, nb] and seq_lens [B] (int32, the tokens each sequence holds;
+    the caller advances them after ``append``).  ``append`` quantises new tokens and pools completed blocks;
+    ``select`` scores the query against the pooled summary and keeps each sequence's kb best history blocks and
+    its last; ``attend`` gathers them through the table.  kb None: every block is attended, nothing is selected.
+    ``read`` gives tokens back as dense rows."""
+    q: torch.Tensor
+    k_pool: torch.Tensor
+    v_pool: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+    block_table: torch.Tensor
+    seq_lens: torch.Tensor
+    kb: Optional[int] = None
+    softmax_scale: Optional[float] = None
+    bufs: Dict[str, torch.Tensor] = field(default_factory=dict)
+
+    def __post_init__(self):
+        B, Hq, d = self.q.shape
+        Hkv, block = self.k_pool.shape[1], self.k_pool.shape[2]
+        nb = self.block_table.shape[1]
+        if self.k_pool.shape[3] != d or self.block_table.shape[0] != B or self.seq_lens.shape != (B,):
+            raise ValueError("q [B,Hq,d], pools [P,Hkv,64,d], block_table [B,nb] and seq_lens [B] do not match")
+        self.nb, self.block = nb, block
+        self.shape = make_shape(B, Hq, Hkv, 1, nb * block, d, block, self.q.dtype)
+        self.idx_stride = 0 if self.kb is None else self.kb + 1
+        if self.softmax_scale is None:
+            self.softmax_scale = 1.0 / math.sqrt(d)
+        dev = _dev(self.q)
+        f32 = torch.float32
+        b = self.bufs
+        if self.kb is not None:
+            b.setdefault("kbar", torch.zeros((B, Hkv, nb, d), dtype=f32, device=dev))
+            b.setdefault("qbar", torch.empty((B, Hkv, d), dtype=f32, device=dev))
+            b.setdefault("scores", torch.empty((B, Hkv, nb), dtype=f32, device=dev))
+            b.setdefault("idx", torch.empty((B, Hkv, self.idx_stride), dtype=torch.int32, device=dev))
+            b.setdefault("count", torch.empty((B, Hkv), dtype=torch.int32, device=dev))
+        ws = bsa_workspace_bytes(BSA_OP_DECODE_QUANT, self.shape, self.idx_stride)
+        b.setdefault("workspace", torch.empty((max(ws, 256),), dtype=torch.uint8, device=dev))
+        b.setdefault("o", torch.empty_like(self.q))
+        b.setdefault("lse", torch.empty((B, Hq), dtype=f32, device=dev))
+
+    def _rows_shape(self, T: int, dtype):
+        s = self.shape
+        return make_shape(s.B, s.Hkv, s.Hkv, T, s.Nk, s.d, s.block, dtype)
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, new_lens: Optional[torch.Tensor] = None, stream=None):
+        """Quantise k_new/v_new [B,Hkv,T,d] (t < new_lens[b]) behind seq_lens[b] tokens; completed blocks are pooled."""
+        s = self.shape
+        if k_new.shape != v_new.shape or k_new.shape[:2] != (s.B, s.Hkv) or k_new.shape[3] != s.d:
+            raise ValueError(f"new keys and values are [{s.B}, {s.Hkv}, T, {s.d}], got {list(k_new.shape)}")
+        bsa_paged_append_quant(self._rows_shape(k_new.shape[2], k_new.dtype), k_new, v_new, self.seq_lens,
+                               self.block_table, self.k_pool, self.v_pool, self.k_exp, self.v_exp,
+                               self.bufs.get("kbar"), new_lens=new_lens, stream=stream)
+
+    def read(self, k_out: torch.Tensor, v_out: torch.Tensor, starts: Optional[torch.Tensor] = None, stream=None):
+        """Tokens starts[b] + t into row t of k_out/v_out [B,Hkv,T,d] (bf16 or fp32), as far as the sequence goes."""
+        s = self.shape
+        if k_out.shape != v_out.shape or k_out.shape[:2] != (s.B, s.Hkv) or k_out.shape[3] != s.d:
+            raise ValueError(f"rows read back are [{s.B}, {s.Hkv}, T, {s.d}], got {list(k_out.shape)}")
+        bsa_paged_read_quant(self._rows_shape(k_out.shape[2], k_out.dtype), self.k_pool, self.v_pool, self.k_exp,
+                             self.v_exp, self.block_table, self.seq_lens, k_out, v_out, starts=starts, stream=stream)
+
+    def select(self, stream=None):
+        b, s = self.bufs, self.shape
+        bsa_score_blocks(s, BSA_SCORE_DECODE, self.q, None, b["kbar"], b["qbar"], None, b["scores"], stream=stream)
+        bsa_topk_select_lens(b["scores"], s.B * s.Hkv, self.nb, self.seq_lens, s.Hkv, self.block, self.kb, b["idx"],
+                             self.idx_stride, b["count"], stream=stream)
+
+    def attend(self, idx: Optional[torch.Tensor] = None, stream=None, with_lse: bool = True):
+        b = self.bufs
+        idx = b.get("idx") if idx is None else idx
+        bsa_sparse_attn_decode_quant(self.shape, self.q, self.k_pool, self.v_pool, self.k_exp, self.v_exp,
+                                     self.block_table, self.seq_lens, idx, 0 if idx is None else idx.shape[-1],
+                                     self.softmax_scale, b["workspace"], b["o"], b["lse"] if with_lse else None,
+                                     stream=stream)
+        return b
+
+    def run(self, stream=None, with_lse: bool = True):
+        if self.kb is not None:
+            self.select(stream)
+        return self.attend(stream=stream, with_lse=with_lse)
