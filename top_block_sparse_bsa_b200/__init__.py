@@ -374,34 +374,53 @@ def bsa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: int = BSA_RO
     return out, float(scale.value)
 
 
-def _same_type(what: str, dtype: torch.dtype, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"{what} takes {dtype}, got {t.dtype}")
+# What the calls below check of a tensor before its pointer goes to the library: its type, that it is dense, and that it
+# lives on the device that the call runs on, the current one.  One pass over each tensor: a decode step is a few
+# microseconds on the device, so the binding counts.
+
+def _at(what: str, t, dtype, device: int):
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(what, t, dtype, device)
+    return t.data_ptr()
 
 
-def _one_device(*tensors) -> None:
-    """The calls run on the current device and its current stream: their tensors live there."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError(f"a tensor on {t.device} in a call on cuda:{here}")
+def _refuse(what: str, t, dtype, device: int):
+    if not t.is_cuda:
+        raise ValueError(f"{what}: libbsa takes device tensors")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} is {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}, the call runs on cuda:{device}")
+    raise ValueError(f"{what}: libbsa takes contiguous tensors")
 
 
-def _token_rows(what: str, x, heads: int, d: int):
-    """Pointer and token stride of x [B, N, heads, d]: dense but for the distance between tokens."""
-    if not x.is_cuda:
-        raise ValueError("libbsa takes device tensors")
-    B, N = x.shape[:2]
-    token = x.stride(1) if N > 1 else (x.stride(0) if B > 1 else heads * d)
-    if x.shape[2:] != (heads, d) or (d > 1 and x.stride(3) != 1) or (heads > 1 and x.stride(2) != d) or \
-            (B > 1 and x.stride(0) != N * token):
-        raise ValueError(f"{what}: [B, N, {heads}, {d}] rows, tokens evenly apart")
-    return ctypes.c_void_p(x.data_ptr()), token
+def _here(stream):
+    """(current device, stream handle on it)."""
+    device = torch._C._cuda_getDevice()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, _stream(stream)
 
 
-def _size(t) -> ctypes.c_size_t:
-    return ctypes.c_size_t(t.numel() * t.element_size() if t is not None else 0)
+def _token_rows(what: str, x, shape: BsaShape, dtype, device: int):
+    """Pointer and token stride of x [B, Nq, Hq+2Hkv, d]: dense but for the distance between tokens."""
+    heads, d = shape.Hq + 2 * shape.Hkv, shape.d
+    size, stride = x.size(), x.stride()
+    if x.dtype is not dtype or x.get_device() != device:
+        _refuse(what, x, dtype, device)
+    if size != (shape.B, shape.Nq, heads, d):
+        raise ValueError(f"{what} is [{shape.B}, {shape.Nq}, {heads}, {d}], got {list(size)}")
+    token = stride[1] if shape.Nq > 1 else (stride[0] if shape.B > 1 else heads * d)
+    if (d > 1 and stride[3] != 1) or (heads > 1 and stride[2] != d) or \
+            (shape.B > 1 and stride[0] != shape.Nq * token):
+        raise ValueError(f"{what}: heads and channels are dense, tokens evenly apart")
+    return x.data_ptr(), token
+
+
+def _size(t) -> int:
+    return t.numel() * t.element_size() if t is not None else 0
 
 
 def bsa_workspace_bytes_norm_rope(shape: BsaShape) -> int:
@@ -411,89 +430,98 @@ def bsa_workspace_bytes_norm_rope(shape: BsaShape) -> int:
 def bsa_qkv_norm_rope(shape: BsaShape, qkv, q_weight, k_weight, eps: float, rope: Optional[BsaRope], positions,
                       q, k, v, stream=None) -> None:
     """Norms, rotation and change to head-major of qkv [B, Nq, Hq+2Hkv, d] (a slice of wider rows may be given)."""
-    _same_type("bsa_qkv_norm_rope", qkv.dtype, q_weight, k_weight, q, k, v)
-    _one_device(qkv, q_weight, k_weight, positions, q, k, v)
-    if positions is not None:
-        _same_type("positions", torch.int32, positions)
-    src, token_stride = _token_rows("qkv", qkv, shape.Hq + 2 * shape.Hkv, shape.d)
-    _check("bsa_qkv_norm_rope", lib.bsa_qkv_norm_rope(
-        ctypes.byref(shape), src, token_stride, _ptr(q_weight), _ptr(k_weight), eps,
-        ctypes.byref(rope) if rope is not None else None, _ptr(positions), _ptr(q), _ptr(k), _ptr(v), _stream(stream)))
+    dev, st = _here(stream)
+    t = qkv.dtype
+    src, token_stride = _token_rows("qkv", qkv, shape, t, dev)
+    code = lib.bsa_qkv_norm_rope(
+        ctypes.byref(shape), src, token_stride, _at("q_weight", q_weight, t, dev), _at("k_weight", k_weight, t, dev),
+        eps, ctypes.byref(rope) if rope is not None else None, _at("positions", positions, torch.int32, dev),
+        _at("q", q, t, dev), _at("k", k, t, dev), _at("v", v, t, dev), st)
+    if code:
+        raise BsaError("bsa_qkv_norm_rope", code)
 
 
 def bsa_qkv_norm_rope_bwd(shape: BsaShape, qkv, q_weight, k_weight, eps: float, rope: Optional[BsaRope], positions,
                           dq, dk, dv, d_qkv, d_q_weight=None, d_k_weight=None, workspace=None, stream=None) -> None:
     """Gradients of qkv and of the norms' weights from fp32 dq, dk, dv."""
-    _same_type("bsa_qkv_norm_rope_bwd", qkv.dtype, q_weight, k_weight, d_qkv)
-    _same_type("the gradients of bsa_qkv_norm_rope_bwd", torch.float32, dq, dk, dv, d_q_weight, d_k_weight)
-    _one_device(qkv, q_weight, k_weight, positions, dq, dk, dv, d_qkv, d_q_weight, d_k_weight, workspace)
-    if positions is not None:
-        _same_type("positions", torch.int32, positions)
-    heads = shape.Hq + 2 * shape.Hkv
-    src, token_stride = _token_rows("qkv", qkv, heads, shape.d)
-    dst, d_token_stride = _token_rows("d_qkv", d_qkv, heads, shape.d)
-    _check("bsa_qkv_norm_rope_bwd", lib.bsa_qkv_norm_rope_bwd(
-        ctypes.byref(shape), src, token_stride, _ptr(q_weight), _ptr(k_weight), eps,
-        ctypes.byref(rope) if rope is not None else None, _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dv), dst,
-        d_token_stride, _ptr(d_q_weight), _ptr(d_k_weight), _ptr(workspace), _size(workspace), _stream(stream)))
+    dev, st = _here(stream)
+    t, f32 = qkv.dtype, torch.float32
+    src, token_stride = _token_rows("qkv", qkv, shape, t, dev)
+    dst, d_token_stride = _token_rows("d_qkv", d_qkv, shape, t, dev)
+    code = lib.bsa_qkv_norm_rope_bwd(
+        ctypes.byref(shape), src, token_stride, _at("q_weight", q_weight, t, dev), _at("k_weight", k_weight, t, dev),
+        eps, ctypes.byref(rope) if rope is not None else None, _at("positions", positions, torch.int32, dev),
+        _at("dq", dq, f32, dev), _at("dk", dk, f32, dev), _at("dv", dv, f32, dev), dst, d_token_stride,
+        _at("d_q_weight", d_q_weight, f32, dev), _at("d_k_weight", d_k_weight, f32, dev),
+        _at("workspace", workspace, torch.uint8, dev), _size(workspace), st)
+    if code:
+        raise BsaError("bsa_qkv_norm_rope_bwd", code)
 
 
-def _quant_pools(what: str, k_pool, v_pool, k_exp, v_exp) -> None:
-    for t in (k_pool, v_pool):
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise ValueError(f"{what}: pools hold e4m3 codes (float8_e4m3fn or uint8), got {t.dtype}")
-    _same_type(what + ": exponents", torch.uint8, k_exp, v_exp)
-    if k_pool.shape != v_pool.shape or k_exp.shape != k_pool.shape[:3] or v_exp.shape != k_exp.shape:
-        raise ValueError(f"{what}: pools [P,Hkv,64,d] and exponents [P,Hkv,64] do not match")
-    _one_device(k_pool, v_pool, k_exp, v_exp)
+def _quant_pools(k_pool, v_pool, k_exp, v_exp, device: int):
+    """Pointers of pools [P,Hkv,64,d] (e4m3 codes) and exponents [P,Hkv,64]."""
+    codes = k_pool.dtype
+    if codes is not torch.float8_e4m3fn and codes is not torch.uint8:
+        raise ValueError(f"pools hold e4m3 codes (float8_e4m3fn or uint8), got {codes}")
+    size = k_pool.size()
+    if v_pool.size() != size or k_exp.size() != size[:3] or v_exp.size() != size[:3]:
+        raise ValueError("pools [P,Hkv,64,d] and exponents [P,Hkv,64] do not match")
+    return (_at("k_pool", k_pool, codes, device), _at("v_pool", v_pool, codes, device),
+            _at("k_exp", k_exp, torch.uint8, device), _at("v_exp", v_exp, torch.uint8, device), size[0])
 
 
 def bsa_paged_append_quant(shape: BsaShape, k_new, v_new, seq_lens, block_table, k_pool, v_pool, k_exp, v_exp,
                            pooled_k=None, new_lens=None, stream=None) -> None:
     """Quantise k_new/v_new [B,Hkv,T,d] into positions seq_lens[b]+t (t < new_lens[b]) of the paged cache; pool
     completed blocks."""
-    _quant_pools("bsa_paged_append_quant", k_pool, v_pool, k_exp, v_exp)
-    _same_type("bsa_paged_append_quant", torch.bfloat16, k_new, v_new)
-    _same_type("lengths and table", torch.int32, seq_lens, new_lens, block_table)
-    _one_device(k_new, v_new, seq_lens, new_lens, block_table, pooled_k)
-    _check("bsa_paged_append_quant", lib.bsa_paged_append_quant(
-        ctypes.byref(shape), _ptr(k_new), _ptr(v_new), _ptr(seq_lens), _ptr(new_lens), _ptr(block_table),
-        int(block_table.shape[-1]), int(k_pool.shape[0]), _ptr(k_pool), _ptr(v_pool), _ptr(k_exp), _ptr(v_exp),
-        _ptr(pooled_k), _stream(stream)))
+    dev, st = _here(stream)
+    i32, bf16 = torch.int32, torch.bfloat16
+    kp, vp, ke, ve, pages = _quant_pools(k_pool, v_pool, k_exp, v_exp, dev)
+    code = lib.bsa_paged_append_quant(
+        ctypes.byref(shape), _at("k_new", k_new, bf16, dev), _at("v_new", v_new, bf16, dev),
+        _at("seq_lens", seq_lens, i32, dev), _at("new_lens", new_lens, i32, dev),
+        _at("block_table", block_table, i32, dev), block_table.size(-1), pages, kp, vp, ke, ve,
+        _at("pooled_k", pooled_k, torch.float32, dev), st)
+    if code:
+        raise BsaError("bsa_paged_append_quant", code)
 
 
 def bsa_paged_read_quant(shape: BsaShape, k_pool, v_pool, k_exp, v_exp, block_table, seq_lens, k_out, v_out,
                          starts=None, stream=None) -> None:
     """Tokens starts[b]+t of the quantised cache as dense rows [B,Hkv,T,d]; rows past a sequence stay as they were."""
-    _quant_pools("bsa_paged_read_quant", k_pool, v_pool, k_exp, v_exp)
-    _same_type("lengths and table", torch.int32, seq_lens, starts, block_table)
-    _same_type("bsa_paged_read_quant", torch.bfloat16 if shape.dtype == BSA_BF16 else torch.float32, k_out, v_out)
-    _one_device(block_table, seq_lens, starts, k_out, v_out)
-    _check("bsa_paged_read_quant", lib.bsa_paged_read_quant(
-        ctypes.byref(shape), _ptr(k_pool), _ptr(v_pool), _ptr(k_exp), _ptr(v_exp), int(k_pool.shape[0]),
-        _ptr(block_table), int(block_table.shape[-1]), _ptr(seq_lens), _ptr(starts), _ptr(k_out), _ptr(v_out),
-        _stream(stream)))
+    dev, st = _here(stream)
+    i32, t = torch.int32, torch.bfloat16 if shape.dtype == BSA_BF16 else torch.float32
+    kp, vp, ke, ve, pages = _quant_pools(k_pool, v_pool, k_exp, v_exp, dev)
+    code = lib.bsa_paged_read_quant(
+        ctypes.byref(shape), kp, vp, ke, ve, pages, _at("block_table", block_table, i32, dev), block_table.size(-1),
+        _at("seq_lens", seq_lens, i32, dev), _at("starts", starts, i32, dev), _at("k_out", k_out, t, dev),
+        _at("v_out", v_out, t, dev), st)
+    if code:
+        raise BsaError("bsa_paged_read_quant", code)
 
 
 def bsa_sparse_attn_decode_quant(shape: BsaShape, q, k_pool, v_pool, k_exp, v_exp, block_table, seq_lens, idx,
                                  idx_stride: int, softmax_scale: float, workspace, o, lse=None, stream=None) -> None:
     """Decode over the quantised paged cache: kept blocks idx [B,Hkv,idx_stride], or every block (None, 0)."""
-    _quant_pools("bsa_sparse_attn_decode_quant", k_pool, v_pool, k_exp, v_exp)
-    _same_type("bsa_sparse_attn_decode_quant", torch.bfloat16, q, o)
-    _same_type("lengths, lists and table", torch.int32, seq_lens, idx, block_table)
-    _one_device(q, block_table, seq_lens, idx, workspace, o, lse)
-    _check("bsa_sparse_attn_decode_quant", lib.bsa_sparse_attn_decode_quant(
-        ctypes.byref(shape), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_exp), _ptr(v_exp), int(k_pool.shape[0]),
-        _ptr(block_table), int(block_table.shape[-1]), _ptr(seq_lens), _ptr(idx), int(idx_stride), softmax_scale,
-        _ptr(workspace), _size(workspace), _ptr(o), _ptr(lse), _stream(stream)))
+    dev, st = _here(stream)
+    i32, bf16 = torch.int32, torch.bfloat16
+    kp, vp, ke, ve, pages = _quant_pools(k_pool, v_pool, k_exp, v_exp, dev)
+    code = lib.bsa_sparse_attn_decode_quant(
+        ctypes.byref(shape), _at("q", q, bf16, dev), kp, vp, ke, ve, pages, _at("block_table", block_table, i32, dev),
+        block_table.size(-1), _at("seq_lens", seq_lens, i32, dev), _at("idx", idx, i32, dev), idx_stride,
+        softmax_scale, _at("workspace", workspace, torch.uint8, dev), _size(workspace), _at("o", o, bf16, dev),
+        _at("lse", lse, torch.float32, dev), st)
+    if code:
+        raise BsaError("bsa_sparse_attn_decode_quant", code)
 
 
 def bsa_topk_select_lens(scores, rows: int, ncols: int, lens, rows_per_len: int, block: int, kb: int, idx_out,
                          idx_stride: int, count_out=None, stream=None) -> None:
     """Decode selection where row r's sequence r // rows_per_len holds lens[r // rows_per_len] tokens."""
-    _same_type("scores", torch.float32, scores)
-    _same_type("lengths and lists", torch.int32, lens, idx_out, count_out)
-    _one_device(scores, lens, idx_out, count_out)
-    _check("bsa_topk_select_lens", lib.bsa_topk_select_lens(
-        _ptr(scores), int(rows), int(ncols), _ptr(lens), int(rows_per_len), int(block), int(kb), _ptr(idx_out),
-        int(idx_stride), _ptr(count_out), _stream(stream)))
+    dev, st = _here(stream)
+    i32 = torch.int32
+    code = lib.bsa_topk_select_lens(
+        _at("scores", scores, torch.float32, dev), rows, ncols, _at("lens", lens, i32, dev), rows_per_len, block, kb,
+        _at("idx_out", idx_out, i32, dev), idx_stride, _at("count_out", count_out, i32, dev), st)
+    if code:
+        raise BsaError("bsa_topk_select_lens", code)

@@ -31,7 +31,8 @@ namespace bsa {
 namespace nrope {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;   // rows a lane has in flight
+constexpr int kUnroll = 4;   // rows a lane of the forward has in flight
+constexpr int kBwdCtasPerSm = 2;
 
 enum { LAYOUT_NONE = 0, LAYOUT_HALF = 1, LAYOUT_PAIRS = 2 };
 
@@ -45,6 +46,26 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
   v[0] = __uint_as_float(t.x << 16); v[1] = __uint_as_float(t.x & 0xFFFF0000u);
   v[2] = __uint_as_float(t.y << 16); v[3] = __uint_as_float(t.y & 0xFFFF0000u);
 }
+// The same, kept as loaded: a bf16 piece waits for its turn in two registers.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 v;
+  __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
+};
 __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -74,20 +95,19 @@ __device__ __forceinline__ Lane lane_channels(int l, int d, int rot) {
   return m;
 }
 
-// The lane's four frequencies as fractions of a turn, 2^64 to the turn.
-__device__ __forceinline__ void lane_freqs(const double* __restrict__ inv_freq, int l, bool rotated,
-                                           unsigned long long (&f)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = 0;
-    if (rotated) {
-      double t = __ldg(inv_freq + 4 * l + i) * 0.15915494309189533577;   // 1 / (2 pi)
-      t -= floor(t);
-      f[i] = __double2ull_rd(t * 18446744073709551616.0);
-    }
+// Frequencies as fractions of a turn, 2^64 to the turn, in shared memory: one
+// conversion a block and pair.  A lane's four begin at 4 l.
+constexpr int kMaxPairs = 128;
+__device__ __forceinline__ void block_freqs(const double* __restrict__ inv_freq, int pairs,
+                                            unsigned long long* __restrict__ f) {
+  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    double t = __ldg(inv_freq + i) * 0.15915494309189533577;   // 1 / (2 pi)
+    t -= floor(t);
+    f[i] = __double2ull_rd(t * 18446744073709551616.0);
   }
+  __syncthreads();
 }
-__device__ __forceinline__ void angles(const unsigned long long (&f)[4], int pos, float scale, float (&c)[4],
+__device__ __forceinline__ void angles(const unsigned long long* __restrict__ f, int pos, float scale, float (&c)[4],
                                        float (&s)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -133,9 +153,10 @@ __device__ __forceinline__ float row_sum(float v) {
 // Work items: token tiles (kThreads/GS tokens, one per lane group) x runs of
 // head_run heads.
 template <typename T, int GS, int LAYOUT>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(const NormRopeArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const NormRopeArgs p) {
   griddep_wait();
   constexpr int kTokens = kThreads / GS;
+  __shared__ unsigned long long freqs[kMaxPairs];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS;
   const Lane m = lane_channels<LAYOUT>(l, p.d, p.rot);
   const int64_t token = static_cast<int64_t>(blockIdx.x) * kTokens + grp;
@@ -148,9 +169,8 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const NormRopeArgs p) {
   const T* row0 = static_cast<const T*>(p.qkv) + tk * p.token_stride;
   float c[4], s[4];
   if (LAYOUT != LAYOUT_NONE && h_begin < p.Hq + p.Hkv) {
-    unsigned long long f[4];
-    lane_freqs(p.inv_freq, l, m.rotated, f);
-    angles(f, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
+    block_freqs(p.inv_freq, p.rot / 2, freqs);
+    if (m.rotated) angles(freqs + 4 * l, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
   }
   for (int part = 0; part < 3; ++part) {   // queries, keys, values
     const int lo = part == 0 ? 0 : (part == 1 ? p.Hq : p.Hq + p.Hkv);
@@ -166,51 +186,57 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const NormRopeArgs p) {
       load4(weight + m.b, wb);
     }
     for (int h0 = from; h0 < to; h0 += kUnroll) {
-      float xa[kUnroll][4], xb[kUnroll][4];
+      Raw<T> ra[kUnroll], rb[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (m.on && live && h0 + u < to) {
-          load4(row0 + static_cast<int64_t>(h0 + u) * p.d + m.a, xa[u]);
-          load4(row0 + static_cast<int64_t>(h0 + u) * p.d + m.b, xb[u]);
+          ra[u].load(row0 + (h0 + u) * p.d + m.a);
+          rb[u].load(row0 + (h0 + u) * p.d + m.b);
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) xa[u][i] = xb[u][i] = 0.0f;
+          ra[u].zero();
+          rb[u].zero();
         }
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
+        float xa[4], xb[4];
+        ra[u].get(xa);
+        rb[u].get(xb);
         if (norm) {
           float ss = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) ss += xa[u][i] * xa[u][i] + xb[u][i] * xb[u][i];
+          for (int i = 0; i < 4; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
           const float r = rsqrtf(row_sum<GS>(ss) * p.inv_d + p.eps);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            xa[u][i] *= r * wa[i];
-            xb[u][i] *= r * wb[i];
+            xa[i] *= r * wa[i];
+            xb[i] *= r * wb[i];
           }
         }
-        if (LAYOUT != LAYOUT_NONE && part < 2 && m.rotated) rotate<LAYOUT>(xa[u], xb[u], c, s);
+        if (LAYOUT != LAYOUT_NONE && part < 2 && m.rotated) rotate<LAYOUT>(xa, xb, c, s);
         if (m.on && live && h0 + u < to) {
           T* dst = out + ((static_cast<int64_t>(b) * heads + (h0 + u - lo)) * p.N + n) * p.d;
-          store4(dst + m.a, xa[u]);
-          store4(dst + m.b, xb[u]);
+          store4(dst + m.a, xa);
+          store4(dst + m.b, xb);
         }
       }
     }
   }
 }
 
-// Backward.  Persistent over (token tile, head run) items; each lane sums the
-// weights' gradients of its channels over all its rows in fp32, the block's
-// groups are added in order at the end, and dw_reduce_kernel adds the blocks
-// in 64 bits: the same order on every run.
+// Backward.  Persistent over (token tile, head run) items.  The weights'
+// gradients of a lane's channels are summed in registers over the heads of a
+// token and added to the lane's own place in shared memory token by token
+// (which frees half of the registers that sums over all rows would hold); the
+// block's groups are added in order at the end, and dw_reduce_kernel adds the
+// blocks in 64 bits: the same order on every run.
 template <typename T, int GS, int LAYOUT>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(const NormRopeArgs p) {
+__global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const NormRopeArgs p) {
   griddep_wait();
   constexpr int kTokens = kThreads / GS;
-  constexpr int kRows = 2;   // rows a lane has in flight (their fp32 gradients and inputs)
-  __shared__ float acc[2][kTokens][GS * 8];
+  constexpr int kRows = sizeof(T) == 2 ? 4 : 2;   // rows a lane has in flight (their fp32 gradients and inputs)
+  __shared__ float4 acc[2][2][kThreads];   // [weight][piece][thread]
+  __shared__ unsigned long long freqs[kMaxPairs];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS;
   const Lane m = lane_channels<LAYOUT>(l, p.d, p.rot);
   const int64_t tokens = static_cast<int64_t>(p.B) * p.N;
@@ -218,9 +244,9 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const NormRopeArgs p) {
   const int H = p.Hq + 2 * p.Hkv;
   const int runs = (H + p.head_run - 1) / p.head_run;
   const bool norm = p.q_weight != nullptr;
-  unsigned long long f[4];
-  if (LAYOUT != LAYOUT_NONE) lane_freqs(p.inv_freq, l, m.rotated, f);
-  float dwa[2][4] = {}, dwb[2][4] = {};
+  if (LAYOUT != LAYOUT_NONE) block_freqs(p.inv_freq, p.rot / 2, freqs);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int64_t item = blockIdx.x; item < tiles * runs; item += gridDim.x) {
     const int64_t tile = item / runs;
     const int run = static_cast<int>(item - tile * runs);
@@ -233,51 +259,56 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const NormRopeArgs p) {
     const T* row0 = static_cast<const T*>(p.qkv) + tk * p.token_stride;
     T* drow0 = static_cast<T*>(p.d_qkv) + tk * p.d_token_stride;
     float c[4], s[4];
-    if (LAYOUT != LAYOUT_NONE && h_begin < p.Hq + p.Hkv) {
-      angles(f, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
+    if (LAYOUT != LAYOUT_NONE && m.rotated && h_begin < p.Hq + p.Hkv) {
+      angles(freqs + 4 * l, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] = -s[i];
     }
-#pragma unroll
     for (int part = 0; part < 3; ++part) {
       const int lo = part == 0 ? 0 : (part == 1 ? p.Hq : p.Hq + p.Hkv);
       const int heads = part == 0 ? p.Hq : p.Hkv;
       const int from = max(h_begin, lo), to = min(h_end, lo + heads);
       if (from >= to) continue;
-      const float* dz = part == 0 ? p.dq : (part == 1 ? p.dk : p.dv);
+      const int64_t head_step = static_cast<int64_t>(p.N) * p.d;
+      const float* dz = (part == 0 ? p.dq : (part == 1 ? p.dk : p.dv)) +
+                        (static_cast<int64_t>(b) * heads - lo) * head_step + static_cast<int64_t>(n) * p.d;
       const T* weight = static_cast<const T*>(part == 0 ? p.q_weight : p.k_weight);
       const bool nm = part < 2 && norm;
-      float wa[4], wb[4];
+      float wa[4] = {}, wb[4] = {}, dwa[4] = {}, dwb[4] = {};
       if (nm && m.on) {
         load4(weight + m.a, wa);
         load4(weight + m.b, wb);
       }
       for (int h0 = from; h0 < to; h0 += kRows) {
-        float ga[kRows][4], gb[kRows][4], xa[kRows][4], xb[kRows][4];
+        Raw<float> ga_[kRows], gb_[kRows];
+        Raw<T> xa_[kRows], xb_[kRows];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          const bool in = m.on && live && h0 + u < to;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ga[u][i] = gb[u][i] = xa[u][i] = xb[u][i] = 0.0f;
-          if (in) {
-            const float* src = dz + ((static_cast<int64_t>(b) * heads + (h0 + u - lo)) * p.N + n) * p.d;
-            load4(src + m.a, ga[u]);
-            load4(src + m.b, gb[u]);
+          ga_[u].zero(), gb_[u].zero(), xa_[u].zero(), xb_[u].zero();
+          if (m.on && live && h0 + u < to) {
+            const float* src = dz + (h0 + u) * head_step;
+            ga_[u].load(src + m.a);
+            gb_[u].load(src + m.b);
             if (nm) {
-              load4(row0 + static_cast<int64_t>(h0 + u) * p.d + m.a, xa[u]);
-              load4(row0 + static_cast<int64_t>(h0 + u) * p.d + m.b, xb[u]);
+              xa_[u].load(row0 + (h0 + u) * p.d + m.a);
+              xb_[u].load(row0 + (h0 + u) * p.d + m.b);
             }
           }
         }
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          if (LAYOUT != LAYOUT_NONE && part < 2 && m.rotated) rotate<LAYOUT>(ga[u], gb[u], c, s);
+          float ga[4], gb[4];
+          ga_[u].get(ga);
+          gb_[u].get(gb);
+          if (LAYOUT != LAYOUT_NONE && part < 2 && m.rotated) rotate<LAYOUT>(ga, gb, c, s);
           if (nm) {
-            float ss = 0.0f, sd = 0.0f;
+            float xa[4], xb[4], ss = 0.0f, sd = 0.0f;
+            xa_[u].get(xa);
+            xb_[u].get(xb);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              ss += xa[u][i] * xa[u][i] + xb[u][i] * xb[u][i];
-              if (m.on) sd += ga[u][i] * wa[i] * xa[u][i] + gb[u][i] * wb[i] * xb[u][i];
+              ss += xa[i] * xa[i] + xb[i] * xb[i];
+              sd += ga[i] * wa[i] * xa[i] + gb[i] * wb[i] * xb[i];
             }
             ss = row_sum<GS>(ss);
             sd = row_sum<GS>(sd);
@@ -285,40 +316,43 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const NormRopeArgs p) {
             const float k = r * r * sd * p.inv_d;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (m.on) {
-                dwa[part & 1][i] += ga[u][i] * xa[u][i] * r;
-                dwb[part & 1][i] += gb[u][i] * xb[u][i] * r;
-                ga[u][i] = r * (ga[u][i] * wa[i] - xa[u][i] * k);
-                gb[u][i] = r * (gb[u][i] * wb[i] - xb[u][i] * k);
-              }
+              dwa[i] += ga[i] * xa[i] * r;
+              dwb[i] += gb[i] * xb[i] * r;
+              ga[i] = r * (ga[i] * wa[i] - xa[i] * k);
+              gb[i] = r * (gb[i] * wb[i] - xb[i] * k);
             }
           }
           if (m.on && live && h0 + u < to) {
-            T* dst = drow0 + static_cast<int64_t>(h0 + u) * p.d;
-            store4(dst + m.a, ga[u]);
-            store4(dst + m.b, gb[u]);
+            T* dst = drow0 + (h0 + u) * p.d;
+            store4(dst + m.a, ga);
+            store4(dst + m.b, gb);
           }
         }
+      }
+      if (nm && live) {
+        float4* mine = &acc[part][0][threadIdx.x];
+        float4 t = mine[0];
+        mine[0] = make_float4(t.x + dwa[0], t.y + dwa[1], t.z + dwa[2], t.w + dwa[3]);
+        t = mine[kThreads];
+        mine[kThreads] = make_float4(t.x + dwb[0], t.y + dwb[1], t.z + dwb[2], t.w + dwb[3]);
       }
     }
   }
   if (!norm) return;
-  if (m.on) {
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[w][grp][m.a + i] = dwa[w][i];
-        acc[w][grp][m.b + i] = dwb[w][i];
-      }
-  }
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * p.d; e += kThreads) {
-    const int w = e / p.d, ch = e - w * p.d;
-    float v = 0.0f;
-#pragma unroll
-    for (int g = 0; g < kTokens; ++g) v += acc[w][g][ch];
-    p.dw_partial[static_cast<int64_t>(blockIdx.x) * 2 * p.d + e] = v;
+  // thread = (weight, piece, lane of the row): its four channels over the groups in order
+  for (int e = threadIdx.x; e < 4 * GS; e += kThreads) {
+    const int w = e / (2 * GS), piece = e / GS % 2, le = e % GS;
+    const Lane me = lane_channels<LAYOUT>(le, p.d, p.rot);
+    if (!me.on) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int g = 0; g < kTokens; ++g) {
+      const float4 t = acc[w][piece][g * GS + le];
+      v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+    }
+    *reinterpret_cast<float4*>(p.dw_partial + static_cast<int64_t>(blockIdx.x) * 2 * p.d + w * p.d +
+                               (piece ? me.b : me.a)) = v;
   }
 }
 
@@ -379,7 +413,7 @@ cudaError_t by_width(const NormRopeArgs& p, bool bwd, int num_sms, cudaStream_t 
 
 }  // namespace nrope
 
-int norm_rope_bwd_blocks(int num_sms) { return 4 * num_sms; }
+int norm_rope_bwd_blocks(int num_sms) { return nrope::kBwdCtasPerSm * num_sms; }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, bool bf16, bool bwd, int num_sms, cudaStream_t st) {
   return bf16 ? nrope::by_width<__nv_bfloat16>(a, bwd, num_sms, st) : nrope::by_width<float>(a, bwd, num_sms, st);

@@ -467,7 +467,8 @@ class QuantDecodeStep:
         B, Hq, d = self.q.shape
         Hkv, block = self.k_pool.shape[1], self.k_pool.shape[2]
         nb = self.block_table.shape[1]
-        if self.k_pool.shape[3] != d or self.block_table.shape[0] != B or self.seq_lens.shape != (B,):
+        if self.k_pool.shape[3] != d or self.block_table.shape[0] != B or self.seq_lens.shape != (B,) or \
+                Hq % Hkv != 0:
             raise ValueError("q [B,Hq,d], pools [P,Hkv,64,d], block_table [B,nb] and seq_lens [B] do not match")
         self.nb, self.block = nb, block
         self.shape = make_shape(B, Hq, Hkv, 1, nb * block, d, block, self.q.dtype)
