@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Quan
 template <int D>
 __global__ void __launch_bounds__(D) combine_kernel(const QuantDecodeArgs p) {
   griddep_wait();
-  __shared__ float red[D / 32];
+  __shared__ float red[D / 32], factor[D];
   const int G = p.Hq / p.Hkv;
   const int b = blockIdx.x / p.Hq, hq = blockIdx.x - b * p.Hq;
   const int g = hq / G, h = hq - g * G;
@@ -464,31 +464,44 @@ __global__ void __launch_bounds__(D) combine_kernel(const QuantDecodeArgs p) {
   const int64_t total = static_cast<int64_t>(p.pre[p.B]) * p.Hkv;
   const int C = ranges(total, p.num_ctas);
   const int64_t x0 = static_cast<int64_t>(before) * p.Hkv + static_cast<int64_t>(g) * w;
-  const int first = cta_of(x0, total, C), last = cta_of(x0 + w - 1, total, C);
-  if (first == last) return;
-  // the row begins in block `first` (slot 1 there unless it begins with the block's range and goes on)
-  auto record = [&](int k) {
-    const int64_t lo = static_cast<int64_t>(k) * total / C;
-    return p.partial + ((static_cast<int64_t>(k) * 2 + (x0 < lo ? 0 : 1)) * G + h) * (D + 4);
-  };
+  const int first = cta_of(x0, total, C), n = cta_of(x0 + w - 1, total, C) - first + 1;
+  if (n == 1) return;
+  // the row begins inside range `first` (its record 1) and goes on in the next ones (their records 0)
+  const float* rec = p.partial + (static_cast<int64_t>(first) * 2 * G + h) * (D + 4);
+  const int step = 2 * G * (D + 4);
+  auto record = [&](int k) { return rec + (k == 0 ? G * (D + 4) : static_cast<int64_t>(k) * step); };
   float mx = -INFINITY;
-  for (int k = first + tid; k <= last; k += D) mx = fmaxf(mx, record(k)[0]);
+  for (int k = tid; k < n; k += D) mx = fmaxf(mx, record(k)[0]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if ((tid & 31) == 0) red[tid >> 5] = mx;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) mx = fmaxf(mx, red[k]);
+  __syncthreads();
+  // records D at a time: thread = record for their factors, then thread = channel
   float L = 0.0f, acc = 0.0f;
-  if (mx != -INFINITY) {
-#pragma unroll 8
-    for (int k = first; k <= last; ++k) {
-      const float* rec = record(k);
-      const float f = exp2f(rec[0] - mx);     // 0 where the record is empty
-      L += f * rec[1];
-      acc += f * rec[4 + tid];
+  for (int k0 = 0; k0 < n; k0 += D) {
+    float f = 0.0f;
+    if (k0 + tid < n && mx != -INFINITY) {
+      const float2 ml = *reinterpret_cast<const float2*>(record(k0 + tid));
+      f = exp2f(ml.x - mx);     // 0 where the record is empty
+      L += f * ml.y;
     }
+    factor[tid] = f;
+    __syncthreads();
+    const int m = min(D, n - k0);
+#pragma unroll 8
+    for (int k = 0; k < m; ++k) acc += factor[k] * record(k0 + k)[4 + tid];
+    __syncthreads();
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if ((tid & 31) == 0) red[tid >> 5] = L;
+  __syncthreads();
+  L = 0.0f;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) L += red[k];
   p.o[orow * D + tid] = __float2bfloat16_rn(mx == -INFINITY ? 0.0f : acc / L);
   if (p.lse && tid == 0) p.lse[orow] = (mx == -INFINITY) ? -INFINITY : (mx - kLift + log2f(L)) * 0.69314718055994530942f;
 }

@@ -357,23 +357,26 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
 }
 
 // dw[e] = the blocks' partial sums, e over both weights' channels: 32 outputs
-// a block, eight threads each, added in 64 bits in a fixed order.
-__global__ void __launch_bounds__(256) dw_reduce_kernel(const float* __restrict__ partial, int blocks, int d,
-                                                        float* __restrict__ dqw, float* __restrict__ dkw) {
+// a block, 32 threads each, added in 64 bits in a fixed order.
+__global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* __restrict__ partial, int blocks, int d,
+                                                         float* __restrict__ dqw, float* __restrict__ dkw) {
   griddep_wait();
-  __shared__ double part[8][32];
+  __shared__ double part[32][33];
   const int col = threadIdx.x % 32, row = threadIdx.x / 32;
   const int e = blockIdx.x * 32 + col;
   double v = 0.0;
-  if (e < 2 * d)
-    for (int k = row; k < blocks; k += 8) v += static_cast<double>(partial[static_cast<int64_t>(k) * 2 * d + e]);
+  if (e < 2 * d) {
+#pragma unroll 8
+    for (int k = row; k < blocks; k += 32) v += static_cast<double>(partial[static_cast<int64_t>(k) * 2 * d + e]);
+  }
   part[row][col] = v;
   __syncthreads();
-  if (row == 0 && e < 2 * d) {
+  // warp `row` takes output `row`: its lanes hold the 32 threads' sums
+  v = part[col][row];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) v += part[k][col];
-    (e < d ? dqw[e] : dkw[e - d]) = static_cast<float>(v);
-  }
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int out = blockIdx.x * 32 + row;
+  if (col == 0 && out < 2 * d) (out < d ? dqw[out] : dkw[out - d]) = static_cast<float>(v);
 }
 
 template <typename T, int GS, int LAYOUT>
@@ -394,7 +397,7 @@ cudaError_t launch(NormRopeArgs p, bool bwd, int num_sms, cudaStream_t st) {
   const int grid = static_cast<int>(items < norm_rope_bwd_blocks(num_sms) ? items : norm_rope_bwd_blocks(num_sms));
   cudaError_t e = launch_dependent(bwd_kernel<T, GS, LAYOUT>, dim3(grid), dim3(kThreads), 0, st, p);
   if (e != cudaSuccess || p.q_weight == nullptr) return e;
-  return launch_dependent(dw_reduce_kernel, dim3((2 * p.d + 31) / 32), dim3(256), 0, st, p.dw_partial, grid, p.d,
+  return launch_dependent(dw_reduce_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, st, p.dw_partial, grid, p.d,
                           p.d_q_weight, p.d_k_weight);
 }
 
