@@ -250,7 +250,7 @@ struct QuantLayout {
 QuantLayout quant_layout(const bsa_shape_t* s, int num_sms) {
   QuantLayout L{};
   const int forced = g_split_override.load(std::memory_order_relaxed);
-  L.num_ctas = forced > 0 ? forced : quant_decode_ctas(num_sms);
+  L.num_ctas = forced > 0 ? forced : quant_decode_ctas(num_sms, s->Hq / s->Hkv);
   size_t off = 0;
   L.pre = off;
   off = align256(off + (static_cast<size_t>(s->B) + 1) * sizeof(int));

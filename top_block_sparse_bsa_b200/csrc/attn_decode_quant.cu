@@ -48,9 +48,16 @@ namespace qdecode {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 2;
 constexpr float kLift = 8.0f;        // weights are 2^(y - M + 8)
 constexpr float kHeadroom = 7.0f;    // M moves when y > M + 7: weights stay below 2^15
+
+// NB = sets of eight query heads a warp carries.  One set leaves the registers
+// for two blocks an SM; two sets (groups of 9 to 16 heads) take one block with
+// twice the stages, and each code is still converted once.
+__host__ __device__ constexpr int ctas_per_sm(int NB) { return NB == 1 ? 2 : 1; }
+__host__ __device__ constexpr int stages(int NB) { return NB == 1 ? 3 : 6; }
+// a stage: 16 key rows, 16 value rows, their exponent bytes
+__host__ __device__ constexpr int stage_bytes(int D) { return 2 * 16 * D + 32; }
 
 __device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two) {
   uint32_t r;
@@ -72,7 +79,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Ranges that `total` positions are cut into: none is empty.
 __device__ __forceinline__ int ranges(int64_t total, int ctas) {
@@ -84,9 +95,9 @@ __device__ __forceinline__ int cta_of(int64_t x, int64_t total, int C) {
   return static_cast<int>(((x + 1) * C + total - 1) / total) - 1;
 }
 
-// pre[b] = list positions of the sequences before b (of one KV head), b <= B:
-// from a list every sequence has list_len positions, without one as many as
-// it has blocks.
+// Without a list, pre[b] = blocks of the sequences before b, b <= B: a
+// sequence has as many positions (of one KV head) as it has blocks.  With one
+// every sequence has list_len positions and nothing is read for the plan.
 __device__ __forceinline__ void plan_positions(const QuantDecodeArgs& p, int* pre, int* warp_sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0;
@@ -95,7 +106,7 @@ __device__ __forceinline__ void plan_positions(const QuantDecodeArgs& p, int* pr
     int w = 0;
     if (b < p.B) {
       const int len = p.lens ? min(max(p.lens[b], 0), p.nb * 64) : p.nb * 64;
-      w = p.idx ? p.list_len : (len + 63) >> 6;
+      w = (len + 63) >> 6;
     }
     int incl = w;
 #pragma unroll
@@ -119,349 +130,427 @@ __device__ __forceinline__ void plan_positions(const QuantDecodeArgs& p, int* pr
   __syncthreads();
 }
 
+// Where 16-byte piece q of a staged row stands, q ^ swizzle(row): eight lanes
+// that read together then meet eight different 16-byte columns.  Keys: two
+// neighbouring rows, four pieces each; values: rows 2c, two pieces each (one,
+// shared by two lanes, where a row is 64 bytes).
 template <int D>
-struct Shared {
-  float o[kWarps][8][D + 4];
-  float m[kWarps][8], l[kWarps][8];
-  int warp_sums[kWarps];
-};
-
-// Where channel pair (r * D/8 + 2 mb) of a head is kept in Shared::o: the
-// pairs of lane r are turned by r/2, so that a warp's stores fill the banks.
+__device__ __forceinline__ int k_swizzle(int row) {
+  return D == 128 ? (row & 1) * 4 : 0;
+}
 template <int D>
-__device__ __forceinline__ int pair_at(int r, int mb) {
-  return r * (D / 8) + 2 * ((mb + (r >> 1)) & (D / 16 - 1));
+__device__ __forceinline__ int v_swizzle(int row) {
+  return D == 128 ? (row & 6) : ((row >> 2) & 1) * 2;
 }
 
+// One row's stretch of list positions inside a block's range.
+struct Item {
+  int b, g, w, t0, t1;
+  int64_t next;      // first position behind it
+};
+
+// The item that begins at position x < hi; b: a sequence not behind x's.
+__device__ __forceinline__ Item item_at(const QuantDecodeArgs& p, const int* pre, int64_t x, int64_t hi, int b) {
+  Item it;
+  int64_t row0;
+  if (p.idx) {
+    it.w = p.list_len;
+    const int bg = static_cast<int>(x / it.w);
+    it.b = bg / p.Hkv;
+    it.g = bg - it.b * p.Hkv;
+    row0 = static_cast<int64_t>(bg) * it.w;
+  } else {
+    while (x >= static_cast<int64_t>(pre[b + 1]) * p.Hkv) ++b;     // passes sequences without a block too
+    it.b = b;
+    it.w = pre[b + 1] - pre[b];
+    const int64_t seq0 = static_cast<int64_t>(pre[b]) * p.Hkv;
+    it.g = static_cast<int>((x - seq0) / it.w);
+    row0 = seq0 + static_cast<int64_t>(it.g) * it.w;
+  }
+  it.t0 = static_cast<int>(x - row0);
+  it.t1 = static_cast<int>(min(hi - row0, static_cast<int64_t>(it.w)));
+  it.next = row0 + it.t1;
+  return it;
+}
+
+// Where channel pair (r * D/8 + 2 mb) of query head 2c or 2c+1 stands among a
+// head's pairs while warps are joined: a warp's stores fill the banks.
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const QuantDecodeArgs p) {
+__device__ __forceinline__ int pair_at(int r, int mb, int c) {
+  return r * (D / 16) + (mb ^ ((2 * c + ((r >> 1) & 1)) & (D / 16 - 1)));
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const QuantDecodeArgs p) {
   constexpr int KH = D / 64;        // 64-byte halves of a row
   constexpr int KS = D / 16;        // k-steps of q . K
   constexpr int MB = D / 16;        // 16-channel row blocks of O
   constexpr int VW = D / 32;        // 32-bit words of a V row per lane
+  constexpr int R = stages(NB);
+  constexpr int SB = stage_bytes(D);
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem_raw);
-  int* pre = reinterpret_cast<int*>(smem_raw + sizeof(Shared<D>));
+  __shared__ float sm_m[kWarps][8 * NB], sm_l[kWarps][8 * NB];
+  __shared__ int sm_slot[kWarps], warp_sums[kWarps];
+  int* pre = reinterpret_cast<int*>(smem_raw + kWarps * R * SB);
   griddep_wait();   // lists, lengths and the cache come from the kernels launched before
-  plan_positions(p, pre, sh.warp_sums);
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= p.B; b += kThreads) p.pre[b] = pre[b];
+  if (p.idx == nullptr) {
+    plan_positions(p, pre, warp_sums);
+    if (blockIdx.x == 0)
+      for (int b = threadIdx.x; b <= p.B; b += kThreads) p.pre[b] = pre[b];
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int G = p.Hq / p.Hkv;
-  const int sets = (G + 7) / 8;                 // warps split into sets of eight query heads each
-  const int per_set = kWarps / sets;
-  const int set = warp / per_set, wi = warp % per_set;
-  const int64_t total = static_cast<int64_t>(pre[p.B]) * p.Hkv;
+  const int64_t total = static_cast<int64_t>(p.idx ? p.B * p.list_len : pre[p.B]) * p.Hkv;
   const int C = ranges(total, gridDim.x);
   if (static_cast<int>(blockIdx.x) >= C) return;
   int64_t x = blockIdx.x * total / C;
   const int64_t hi = (blockIdx.x + 1) * total / C;
-  int b = 0;
-  if (x < hi) {   // the sequence of position x: the last b with pre[b] * Hkv <= x
-    int lo_b = 0, hi_b = p.B;
-    while (hi_b - lo_b > 1) {
-      const int mid = (lo_b + hi_b) / 2;
-      if (static_cast<int64_t>(pre[mid]) * p.Hkv <= x) lo_b = mid; else hi_b = mid;
+  int b_first = 0;
+  if (p.idx == nullptr) {   // the sequence of position x: the last b with pre[b] * Hkv <= x
+    int hi_b = p.B;
+    while (hi_b - b_first > 1) {
+      const int mid = (b_first + hi_b) / 2;
+      if (static_cast<int64_t>(pre[mid]) * p.Hkv <= x) b_first = mid; else hi_b = mid;
     }
-    b = lo_b;
   }
-  while (x < hi) {
-    const int w = pre[b + 1] - pre[b];
-    const int64_t seq0 = static_cast<int64_t>(pre[b]) * p.Hkv;
-    if (w == 0 || x >= seq0 + static_cast<int64_t>(w) * p.Hkv) {
-      ++b;
-      continue;
-    }
-    const int g = static_cast<int>((x - seq0) / w);
-    const int64_t row0 = seq0 + static_cast<int64_t>(g) * w;     // the row's first position
-    const int t0 = static_cast<int>(x - row0);
-    const int t1 = static_cast<int>(min(hi - row0, static_cast<int64_t>(w)));
-    x = row0 + t1;
-    const int bg = b * p.Hkv + g;
-    const int len = p.lens ? min(max(p.lens[b], 0), p.nb * 64) : p.nb * 64;
-    const int* list = p.idx ? p.idx + static_cast<int64_t>(bg) * p.list_len : nullptr;
-    const int* table = p.table + static_cast<int64_t>(b) * p.table_stride;
 
-    // ---- the query heads of this warp's set, scaled by a power of two into fp16
-    uint32_t qf[KS][2];
-    float qs[2];        // logit factors of heads 2c, 2c+1 of the set
-    {
-      const int h = set * 8 + r;
-      uint32_t raw[KS][2];
+  // ---- the loading side, R chunks ahead of the other: an item's chunks of 16 keys go to the warps in turn, a warp
+  // looks 32 of its own up at once (one a lane), and runs on into the block's next items by itself
+  uint8_t* ring = smem_raw + warp * R * SB;
+  const uint32_t ring_u32 = smem_u32(ring);
+  Item li = item_at(p, pre, x, hi, b_first);   // item being loaded
+  int l_no = 0;                                 // its number
+  int l_base = warp - 32 * kWarps;              // first chunk of the batch held
+  int l_len = 0;
+  unsigned l_left = 0u;                         // lanes whose chunk is still to be taken
+  int my_row = 0, my_n = 0;                     // the lane's chunk: row of 16 in the pools, keys that count
+  int meta = -1;                                // lane s: stage s's item number * 32 + keys, or -1
+  auto seq_len = [&](int b) { return p.lens ? min(max(__ldg(p.lens + b), 0), p.nb * 64) : p.nb * 64; };
+  l_len = seq_len(li.b);
+  auto refill = [&](int slot) {
+    bool have = true;
+    while (l_left == 0u) {
+      l_base += 32 * kWarps;
+      if (l_base >= 4 * (li.t1 - li.t0)) {
+        if (li.next >= hi) {
+          have = false;
+          l_base -= 32 * kWarps;
+          break;
+        }
+        li = item_at(p, pre, li.next, hi, li.b);
+        l_len = seq_len(li.b);
+        ++l_no;
+        l_base = warp;
+      }
+      const int u = l_base + lane * kWarps;
+      my_n = 0;
+      if (u < 4 * (li.t1 - li.t0)) {
+        const int t = li.t0 + (u >> 2);
+        const int blk = p.idx ? __ldg(p.idx + (static_cast<int64_t>(li.b) * p.Hkv + li.g) * p.list_len + t) : t;
+        const int pos = blk * 64 + (u & 3) * 16;
+        if (blk >= p.nb) {
+          atomicOr(p.status, BSA_DEV_BAD_INDEX);
+        } else if (blk >= 0 && pos < l_len) {
+          const int page = __ldg(p.table + static_cast<int64_t>(li.b) * p.table_stride + blk);
+          if (page < 0 || page >= p.num_pages) {
+            atomicOr(p.status, BSA_DEV_BAD_INDEX);
+          } else {
+            my_n = min(16, l_len - pos);
+            my_row = (page * p.Hkv + li.g) * 4 + (u & 3);
+          }
+        }
+      }
+      l_left = __ballot_sync(0xffffffffu, my_n > 0);
+    }
+    int said = -1;
+    if (have) {
+      const int src = __ffs(l_left) - 1;
+      l_left &= l_left - 1;
+      const int row = __shfl_sync(0xffffffffu, my_row, src);
+      said = l_no * 32 + __shfl_sync(0xffffffffu, my_n, src);
+      const uint32_t dst = ring_u32 + slot * SB;
+      const uint8_t* k = p.k_pool + static_cast<int64_t>(row) * (16 * D);
+      const uint8_t* v = p.v_pool + static_cast<int64_t>(row) * (16 * D);
+      constexpr int PR = D / 16;      // 16-byte pieces of a row
+#pragma unroll
+      for (int i = 0; i < PR / 2; ++i) {
+        const int e = i * 32 + lane, rr = e / PR, q = e % PR;
+        cp_async16(dst + rr * D + (q ^ k_swizzle<D>(rr)) * 16, k + e * 16);
+        cp_async16(dst + 16 * D + rr * D + (q ^ v_swizzle<D>(rr)) * 16, v + e * 16);
+      }
+      if (lane < 2) cp_async16(dst + 32 * D + lane * 16, (lane ? p.v_exp : p.k_exp) + static_cast<int64_t>(row) * 16);
+    }
+    cp_async_commit();
+    if (lane == slot) meta = said;
+  };
+  for (int s = 0; s < R; ++s) refill(s);
+
+  int head = 0;               // stage to be taken next
+  int b = b_first;
+  for (int no = 0; x < hi; ++no) {
+    const Item it = item_at(p, pre, x, hi, b);
+    b = it.b;
+    x = it.next;
+    // ---- the group's query heads, scaled by a power of two into fp16: a head's largest value goes to
+    // [2^10, 2^11), smaller ones keep their eight bits down to 2^-25 of it
+    uint32_t qf[NB][KS][2];
+    float qs[NB][2];        // logit factors of heads 2c, 2c+1 of each set
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int h = nb * 8 + r;
+      const __nv_bfloat16* qrow = p.q + (static_cast<int64_t>(b) * p.Hq + it.g * G + h) * D;
       float amax = 0.0f;
-      const __nv_bfloat16* qrow = p.q + (static_cast<int64_t>(b) * p.Hq + g * G + h) * D;
 #pragma unroll
       for (int hf = 0; hf < KH; ++hf)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (h < G) v = __ldg(reinterpret_cast<const uint4*>(qrow + hf * 64 + c * 16 + 8 * i));
-          raw[hf * 4 + 2 * i][0] = v.x;
-          raw[hf * 4 + 2 * i][1] = v.y;
-          raw[hf * 4 + 2 * i + 1][0] = v.z;
-          raw[hf * 4 + 2 * i + 1][1] = v.w;
+          const uint4 v = h < G ? __ldg(reinterpret_cast<const uint4*>(qrow + hf * 64 + c * 16 + 8 * i))
+                                : make_uint4(0, 0, 0, 0);
+          qf[nb][hf * 4 + 2 * i][0] = v.x;
+          qf[nb][hf * 4 + 2 * i][1] = v.y;
+          qf[nb][hf * 4 + 2 * i + 1][0] = v.z;
+          qf[nb][hf * 4 + 2 * i + 1][1] = v.w;
         }
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[k][i] << 16)),
-                                   fabsf(__uint_as_float(raw[k][i] & 0xFFFF0000u))));
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qf[nb][k][i] << 16)),
+                                   fabsf(__uint_as_float(qf[nb][k][i] & 0xFFFF0000u))));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // the head's largest value goes to [2^10, 2^11): smaller ones keep their eight bits down to 2^-25 of it
       const int E = max(static_cast<int>(__float_as_uint(amax) >> 23), 11);
       const float up = __uint_as_float(static_cast<uint32_t>(264 - E) << 23);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          qf[k][i] = pack_f16x2(__uint_as_float(raw[k][i] << 16) * up, __uint_as_float(raw[k][i] & 0xFFFF0000u) * up);
+          qf[nb][k][i] = pack_f16x2(__uint_as_float(qf[nb][k][i] << 16) * up,
+                                    __uint_as_float(qf[nb][k][i] & 0xFFFF0000u) * up);
       const float down = __uint_as_float(static_cast<uint32_t>(E - 10) << 23) * p.scale_log2;
-      qs[0] = __shfl_sync(0xffffffffu, down, (2 * c) * 4);
-      qs[1] = __shfl_sync(0xffffffffu, down, (2 * c + 1) * 4);
+      qs[nb][0] = __shfl_sync(0xffffffffu, down, (2 * c) * 4);
+      qs[nb][1] = __shfl_sync(0xffffffffu, down, (2 * c + 1) * 4);
     }
 
-    float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    float O[MB][4];
+    float M[NB][2], l[NB][2], O[NB][MB][4];
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
+    for (int nb = 0; nb < NB; ++nb) {
+      M[nb][0] = M[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) O[m][i] = 0.0f;
-
-    // ---- chunks of 16 keys: this warp's are wi, wi + per_set, ...; 32 of them are looked up at once, one a lane
-    const int chunks = 4 * (t1 - t0);
-    int base = wi - 32 * per_set;        // first chunk of the batch held
-    unsigned left = 0u;                  // lanes whose chunk is still to be taken
-    int my_row = 0, my_n = 0;            // the lane's chunk: row of 16 in the pools, keys that count
-    int row = 0, n = 0;                  // the chunk that the loads below are for
-    auto next = [&]() -> bool {
-      while (left == 0u) {
-        base += 32 * per_set;
-        if (base >= chunks) return false;
-        const int u = base + lane * per_set;
-        my_n = 0;
-        if (u < chunks) {
-          const int t = t0 + (u >> 2);
-          const int blk = list ? __ldg(list + t) : t;
-          const int pos = blk * 64 + (u & 3) * 16;
-          if (blk >= p.nb) {
-            atomicOr(p.status, BSA_DEV_BAD_INDEX);
-          } else if (blk >= 0 && pos < len) {
-            const int page = __ldg(table + blk);
-            if (page < 0 || page >= p.num_pages) {
-              atomicOr(p.status, BSA_DEV_BAD_INDEX);
-            } else {
-              my_n = min(16, len - pos);
-              my_row = (page * p.Hkv + g) * 4 + (u & 3);
-            }
-          }
-        }
-        left = __ballot_sync(0xffffffffu, my_n > 0);
-      }
-      const int src = __ffs(left) - 1;
-      left &= left - 1;
-      row = __shfl_sync(0xffffffffu, my_row, src);
-      n = __shfl_sync(0xffffffffu, my_n, src);
-      return true;
-    };
-    uint4 kr[2][KH];          // rows r, r+8: 16 bytes of each half
-    uint32_t vr[4][VW];       // rows 2c, 2c+1, 2c+8, 2c+9: D/8 bytes at r * D/8
-    uint32_t ex = 0u;         // lane < 16: key exponent of row `lane`; else value exponent of row lane - 16
-    auto load_k = [&]() {
-      const uint8_t* k = p.k_pool + static_cast<int64_t>(row) * (16 * D);
+      for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int hf = 0; hf < KH; ++hf) kr[i][hf] = ld_stream(k + (r + 8 * i) * D + hf * 64 + c * 16);
-      const uint8_t* e = lane < 16 ? p.k_exp : p.v_exp;
-      ex = __ldg(e + static_cast<int64_t>(row) * 16 + (lane & 15));
-    };
-    auto load_v = [&]() {
-      const uint8_t* v = p.v_pool + static_cast<int64_t>(row) * (16 * D);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* src = v + (2 * c + (i & 1) + 8 * (i >> 1)) * D + r * (D / 8);
-        if constexpr (D == 128) {
-          const uint4 t = ld_stream(src);
-          vr[i][0] = t.x, vr[i][1] = t.y, vr[i][2] = t.z, vr[i][3] = t.w;
-        } else {
-          const uint2 t = __ldg(reinterpret_cast<const uint2*>(src));
-          vr[i][0] = t.x, vr[i][1] = t.y;
-        }
-      }
-    };
-
-    bool more = next();
-    if (more) {
-      load_k();
-      load_v();
+        for (int i = 0; i < 4; ++i) O[nb][m][i] = 0.0f;
     }
-    while (more) {
-      const int cur_n = n;
+    int spare = -1;        // the item's last stage, kept back for the join
+    for (;;) {
+      const int said = __shfl_sync(0xffffffffu, meta, head);
+      if (said < 0 || (said >> 5) != no) break;
+      if (spare >= 0) refill(spare);
+      const int n = said & 31;
+      cp_async_wait_group<R - 1>();
+      __syncwarp();
+      const uint8_t* st = ring + head * SB;
       // ---- S = K q^T: rows r, r+8 x heads 2c, 2c+1
-      float S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float S[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[nb][0] = S[nb][1] = S[nb][2] = S[nb][3] = 0.0f;
 #pragma unroll
       for (int hf = 0; hf < KH; ++hf) {
-        const uint32_t a[4] = {kr[0][hf].x, kr[0][hf].y, kr[0][hf].z, kr[0][hf].w};
-        const uint32_t e[4] = {kr[1][hf].x, kr[1][hf].y, kr[1][hf].z, kr[1][hf].w};
+        const uint4 ka = *reinterpret_cast<const uint4*>(st + r * D + ((hf * 4 + c) ^ k_swizzle<D>(r)) * 16);
+        const uint4 kb = *reinterpret_cast<const uint4*>(st + (r + 8) * D + ((hf * 4 + c) ^ k_swizzle<D>(r + 8)) * 16);
+        const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w};
+        const uint32_t e[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma16816(S, cvt_e4m3x2(a[i]), cvt_e4m3x2(e[i]), cvt_e4m3x2(a[i] >> 16), cvt_e4m3x2(e[i] >> 16),
-                   qf[hf * 4 + i][0], qf[hf * 4 + i][1]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = cvt_e4m3x2(a[i]), a1 = cvt_e4m3x2(e[i]), a2 = cvt_e4m3x2(a[i] >> 16),
+                         a3 = cvt_e4m3x2(e[i] >> 16);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            mma16816(S[nb], a0, a1, a2, a3, qf[nb][hf * 4 + i][0], qf[nb][hf * 4 + i][1]);
+        }
       }
-      const uint32_t cur_ex = ex;
-      more = next();
-      if (more) load_k();
       // ---- weights
-      float wgt[4];
-      {
-        float y[4], back[2];
+      float kf[2], vb[2], back[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = r + 8 * i;
+        uint32_t ke = st[32 * D + key], ve = st[32 * D + 16 + key];
+        if (key >= n) ke = ve = 127u;
+        kf[i] = __uint_as_float(ke << 23);
+        vb[i] = static_cast<float>(static_cast<int>(ve) - 127);
+        back[i] = __uint_as_float((254u - ve) << 23);
+      }
+      uint32_t wb[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float y[4];
         bool high = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int key = r + 8 * i;
-          const bool in = key < cur_n;
-          uint32_t ka = __shfl_sync(0xffffffffu, cur_ex, key);
-          uint32_t va = __shfl_sync(0xffffffffu, cur_ex, 16 + key);
-          if (!in) ka = va = 127u;
-          const float kf = __uint_as_float(ka << 23);
-          const float vb = static_cast<float>(static_cast<int>(va) - 127);
-          back[i] = __uint_as_float((254u - va) << 23);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float v = S[2 * i + h] * kf * qs[h] + vb;
-            y[2 * i + h] = in ? v : -INFINITY;
-            high |= y[2 * i + h] > M[h] + kHeadroom;
+            const float v = S[nb][2 * i + h] * kf[i] * qs[nb][h] + vb[i];
+            y[2 * i + h] = r + 8 * i < n ? v : -INFINITY;
+            high |= y[2 * i + h] > M[nb][h] + kHeadroom;
           }
-        }
         if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float t = fmaxf(y[h], y[2 + h]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-            const float m_new = fmaxf(M[h], t);
-            const float a = (m_new == -INFINITY) ? 1.0f : fast_exp2(M[h] - m_new);
-            M[h] = m_new;
-            l[h] *= a;
+            const float m_new = fmaxf(M[nb][h], t);
+            const float a = (m_new == -INFINITY) ? 1.0f : fast_exp2(M[nb][h] - m_new);
+            M[nb][h] = m_new;
+            l[nb][h] *= a;
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
-              O[m][h] *= a;
-              O[m][2 + h] *= a;
+              O[nb][m][h] *= a;
+              O[nb][m][2 + h] *= a;
             }
           }
         }
+        float wgt[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float ref = (M[h] == -INFINITY) ? 0.0f : kLift - M[h];
+          const float ref = (M[nb][h] == -INFINITY) ? 0.0f : kLift - M[nb][h];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             wgt[2 * i + h] = fast_exp2(y[2 * i + h] + ref);
-            l[h] += wgt[2 * i + h] * back[i];
+            l[nb][h] += wgt[2 * i + h] * back[i];
           }
         }
+        // keys x heads -> heads x keys: the B operand of O^T = V^T w
+        wb[nb][0] = transpose8x8(pack_f16x2(wgt[0], wgt[1]));
+        wb[nb][1] = transpose8x8(pack_f16x2(wgt[2], wgt[3]));
       }
-      // keys x heads -> heads x keys: the B operand of O^T = V^T w
-      const uint32_t b0 = transpose8x8(pack_f16x2(wgt[0], wgt[1]));
-      const uint32_t b1 = transpose8x8(pack_f16x2(wgt[2], wgt[3]));
-      if (cur_n < 16) {   // rows past the sequence may hold anything: a zero weight does not silence a NaN
+      uint32_t vr[4][VW];       // rows 2c, 2c+1, 2c+8, 2c+9: D/8 bytes at r * D/8
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (2 * c + (i & 1) + 8 * (i >> 1) >= cur_n)
+      for (int i = 0; i < 4; ++i) {
+        const int row = 2 * c + (i & 1) + 8 * (i >> 1);
+        const uint8_t* src = st + 16 * D + row * D;
+        if constexpr (D == 128) {
+          const uint4 t = *reinterpret_cast<const uint4*>(src + (r ^ v_swizzle<D>(row)) * 16);
+          vr[i][0] = t.x, vr[i][1] = t.y, vr[i][2] = t.z, vr[i][3] = t.w;
+        } else {
+          const uint2 t = *reinterpret_cast<const uint2*>(src + ((r >> 1) ^ v_swizzle<D>(row)) * 16 + (r & 1) * 8);
+          vr[i][0] = t.x, vr[i][1] = t.y;
+        }
+        if (row >= n) {   // rows past the sequence may hold anything: a zero weight does not silence a NaN
 #pragma unroll
-            for (int k = 0; k < VW; ++k) vr[i][k] = 0u;
+          for (int k = 0; k < VW; ++k) vr[i][k] = 0u;
+        }
       }
 #pragma unroll
       for (int k = 0; k < VW; ++k) {
         // bytes of two keys side by side: channels (0,1) and (2,3) of this word
         const uint32_t lo01 = __byte_perm(vr[0][k], vr[1][k], 0x5140), lo23 = __byte_perm(vr[0][k], vr[1][k], 0x7362);
         const uint32_t hi01 = __byte_perm(vr[2][k], vr[3][k], 0x5140), hi23 = __byte_perm(vr[2][k], vr[3][k], 0x7362);
-        mma16816(O[2 * k], cvt_e4m3x2(lo01), cvt_e4m3x2(lo01 >> 16), cvt_e4m3x2(hi01), cvt_e4m3x2(hi01 >> 16), b0, b1);
-        mma16816(O[2 * k + 1], cvt_e4m3x2(lo23), cvt_e4m3x2(lo23 >> 16), cvt_e4m3x2(hi23), cvt_e4m3x2(hi23 >> 16), b0,
-                 b1);
+        const uint32_t a[2][4] = {{cvt_e4m3x2(lo01), cvt_e4m3x2(lo01 >> 16), cvt_e4m3x2(hi01), cvt_e4m3x2(hi01 >> 16)},
+                                  {cvt_e4m3x2(lo23), cvt_e4m3x2(lo23 >> 16), cvt_e4m3x2(hi23), cvt_e4m3x2(hi23 >> 16)}};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            mma16816(O[nb][2 * k + u], a[u][0], a[u][1], a[u][2], a[u][3], wb[nb][0], wb[nb][1]);
       }
-      if (more) load_v();
+      __syncwarp();
+      spare = head;
+      head = head + 1 == R ? 0 : head + 1;
     }
 
-    // ---- join the warps of each set, then write the row or its partial record
+    // ---- join the warps, then write the row or its partial record; a warp's O waits in its spare stage
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-    if (r == 0) {
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nb][h] += __shfl_xor_sync(0xffffffffu, l[nb][h], o);
         // a NaN logit leaves M as it is; without another key the row must still not pass for an empty one
-        if (M[h] == -INFINITY && l[h] != l[h]) M[h] = 0.0f;
-        sh.m[warp][2 * c + h] = M[h];
-        sh.l[warp][2 * c + h] = l[h];
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(&sh.o[warp][2 * c + h][pair_at<D>(r, m)]) = make_float2(O[m][h], O[m][2 + h]);
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == w;
-    const int slot = t0 > 0 ? 0 : 1;
-    for (int e = threadIdx.x; e < G * (D / 2); e += kThreads) {
-      const int h = e / (D / 2), pr = e - h * (D / 2);         // query head of the group, channel pair
-      const int hs = h >> 3, hh = h & 7;
-      const int at = pair_at<D>(pr / (D / 16), pr % (D / 16));
-      float mx = -INFINITY;
-      for (int k = 0; k < per_set; ++k) mx = fmaxf(mx, sh.m[hs * per_set + k][hh]);
-      float L = 0.0f, o0 = 0.0f, o1 = 0.0f;
-      for (int k = 0; k < per_set; ++k) {
-        const int wk = hs * per_set + k;
-        const float mk = sh.m[wk][hh];
-        if (mk == -INFINITY) continue;
-        const float f = exp2f(mk - mx);
-        const float2 v = *reinterpret_cast<const float2*>(&sh.o[wk][hh][at]);
-        L += f * sh.l[wk][hh];
-        o0 += f * v.x;
-        o1 += f * v.y;
-      }
-      const int64_t orow = static_cast<int64_t>(b) * p.Hq + g * G + h;
-      if (whole) {
-        const float inv = (mx == -INFINITY) ? 0.0f : 1.0f / L;
-        reinterpret_cast<uint32_t*>(p.o + orow * D)[pr] = pack_bf16x2(o0 * inv, o1 * inv);
-        if (p.lse && pr == 0)
-          p.lse[orow] = (mx == -INFINITY) ? -INFINITY : (mx - kLift + log2f(L)) * 0.69314718055994530942f;
-      } else {
-        float* rec = p.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * G + h) * (D + 4);
-        *reinterpret_cast<float2*>(rec + 4 + 2 * pr) = make_float2(o0, o1);
-        if (pr == 0) {
-          rec[0] = mx;
-          rec[1] = L;
+        if (M[nb][h] == -INFINITY && l[nb][h] != l[nb][h]) M[nb][h] = 0.0f;
+        if (r == 0) {
+          sm_m[warp][nb * 8 + 2 * c + h] = M[nb][h];
+          sm_l[warp][nb * 8 + 2 * c + h] = l[nb][h];
         }
       }
     }
-    __syncthreads();
+    if (lane == 0) sm_slot[warp] = spare;
+    const bool whole = it.t0 == 0 && it.t1 == it.w;
+    const int slot = it.t0 > 0 ? 0 : 1;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      if (spare >= 0) {
+        float2* mine = reinterpret_cast<float2*>(ring + spare * SB);
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mine[(2 * c + h) * (D / 2) + pair_at<D>(r, m, c)] = make_float2(O[nb][m][h], O[nb][m][2 + h]);
+      }
+      __syncthreads();
+      const int heads = min(8, G - nb * 8);
+      for (int e = threadIdx.x; e < heads * (D / 2); e += kThreads) {
+        const int h = e / (D / 2), pr = e - h * (D / 2);         // query head of the set, channel pair
+        const int at = h * (D / 2) + pair_at<D>(pr / (D / 16), pr % (D / 16), h >> 1);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, sm_m[k][nb * 8 + h]);
+        float L = 0.0f, o0 = 0.0f, o1 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float mk = sm_m[k][nb * 8 + h];
+          if (mk == -INFINITY) continue;      // a warp without a key: it may have no spare stage
+          const float f = exp2f(mk - mx);
+          const float2 v = reinterpret_cast<const float2*>(smem_raw + (k * R + sm_slot[k]) * SB)[at];
+          L += f * sm_l[k][nb * 8 + h];
+          o0 += f * v.x;
+          o1 += f * v.y;
+        }
+        const int64_t orow = static_cast<int64_t>(b) * p.Hq + it.g * G + nb * 8 + h;
+        if (whole) {
+          const float inv = (mx == -INFINITY) ? 0.0f : 1.0f / L;
+          reinterpret_cast<uint32_t*>(p.o + orow * D)[pr] = pack_bf16x2(o0 * inv, o1 * inv);
+          if (p.lse && pr == 0)
+            p.lse[orow] = (mx == -INFINITY) ? -INFINITY : (mx - kLift + log2f(L)) * 0.69314718055994530942f;
+        } else {
+          float* rec = p.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * G + nb * 8 + h) * (D + 4);
+          *reinterpret_cast<float2*>(rec + 4 + 2 * pr) = make_float2(o0, o1);
+          if (pr == 0) {
+            rec[0] = mx;
+            rec[1] = L;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (spare >= 0) refill(spare);
   }
 }
 
 // One block per (sequence, query head): rows cut by range borders are joined
 // from their records, rows without a key become zero; rows that one range
-// held are complete already.
-template <int D>
-__global__ void __launch_bounds__(D) combine_kernel(const QuantDecodeArgs p) {
+// held are complete already.  Latency is all: eight records (M, l and this
+// thread's channel of O) are asked for at once and folded into a running
+// (M, l, O), and where a row has many records PARTS threads a channel share
+// them.
+template <int D, int PARTS>
+__global__ void __launch_bounds__(D * PARTS) combine_kernel(const QuantDecodeArgs p) {
   griddep_wait();
-  __shared__ float red[D / 32], factor[D];
+  __shared__ float part_m[PARTS], part_l[PARTS], part_o[PARTS][D];
   const int G = p.Hq / p.Hkv;
   const int b = blockIdx.x / p.Hq, hq = blockIdx.x - b * p.Hq;
   const int g = hq / G, h = hq - g * G;
-  const int tid = threadIdx.x;
+  const int ch = threadIdx.x % D, part = threadIdx.x / D;
   const int64_t orow = blockIdx.x;
-  const int before = p.pre[b], w = p.pre[b + 1] - before;
+  const int before = p.idx ? b * p.list_len : p.pre[b], w = p.idx ? p.list_len : p.pre[b + 1] - before;
+  const int64_t total = static_cast<int64_t>(p.idx ? p.B * p.list_len : p.pre[p.B]) * p.Hkv;
   if (w == 0) {
-    p.o[orow * D + tid] = __float2bfloat16_rn(0.0f);
-    if (p.lse && tid == 0) p.lse[orow] = -INFINITY;
+    if (part == 0) p.o[orow * D + ch] = __float2bfloat16_rn(0.0f);
+    if (p.lse && threadIdx.x == 0) p.lse[orow] = -INFINITY;
     return;
   }
-  const int64_t total = static_cast<int64_t>(p.pre[p.B]) * p.Hkv;
   const int C = ranges(total, p.num_ctas);
   const int64_t x0 = static_cast<int64_t>(before) * p.Hkv + static_cast<int64_t>(g) * w;
   const int first = cta_of(x0, total, C), n = cta_of(x0 + w - 1, total, C) - first + 1;
@@ -469,59 +558,76 @@ __global__ void __launch_bounds__(D) combine_kernel(const QuantDecodeArgs p) {
   // the row begins inside range `first` (its record 1) and goes on in the next ones (their records 0)
   const float* rec = p.partial + (static_cast<int64_t>(first) * 2 * G + h) * (D + 4);
   const int step = 2 * G * (D + 4);
-  auto record = [&](int k) { return rec + (k == 0 ? G * (D + 4) : static_cast<int64_t>(k) * step); };
-  float mx = -INFINITY;
-  for (int k = tid; k < n; k += D) mx = fmaxf(mx, record(k)[0]);
+  float M = -INFINITY, L = 0.0f, acc = 0.0f;
+  for (int k0 = part; k0 < n; k0 += 8 * PARTS) {
+    float2 ml[8];
+    float o[8];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if ((tid & 31) == 0) red[tid >> 5] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) mx = fmaxf(mx, red[k]);
-  __syncthreads();
-  // records D at a time: thread = record for their factors, then thread = channel
-  float L = 0.0f, acc = 0.0f;
-  for (int k0 = 0; k0 < n; k0 += D) {
-    float f = 0.0f;
-    if (k0 + tid < n && mx != -INFINITY) {
-      const float2 ml = *reinterpret_cast<const float2*>(record(k0 + tid));
-      f = exp2f(ml.x - mx);     // 0 where the record is empty
-      L += f * ml.y;
+    for (int i = 0; i < 8; ++i) {
+      const int k = k0 + i * PARTS;
+      const float* at = rec + (k == 0 ? G * (D + 4) : static_cast<int64_t>(k) * step);
+      ml[i] = k < n ? *reinterpret_cast<const float2*>(at) : make_float2(-INFINITY, 0.0f);
+      o[i] = k < n ? at[4 + ch] : 0.0f;
     }
-    factor[tid] = f;
-    __syncthreads();
-    const int m = min(D, n - k0);
-#pragma unroll 8
-    for (int k = 0; k < m; ++k) acc += factor[k] * record(k0 + k)[4 + tid];
-    __syncthreads();
+    float m_new = M;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m_new = fmaxf(m_new, ml[i].x);
+    if (m_new == -INFINITY) continue;
+    const float a = exp2f(M - m_new);
+    L *= a;
+    acc *= a;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = exp2f(ml[i].x - m_new);     // 0 where the record is empty
+      L += f * ml[i].y;
+      acc += f * o[i];
+    }
+    M = m_new;
   }
+  if constexpr (PARTS > 1) {
+    if (ch == 0) {
+      part_m[part] = M;
+      part_l[part] = L;
+    }
+    part_o[part][ch] = acc;
+    __syncthreads();
+    if (part > 0) return;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if ((tid & 31) == 0) red[tid >> 5] = L;
-  __syncthreads();
-  L = 0.0f;
+    for (int k = 1; k < PARTS; ++k) M = fmaxf(M, part_m[k]);
+    L = acc = 0.0f;
+    if (M != -INFINITY) {
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) L += red[k];
-  p.o[orow * D + tid] = __float2bfloat16_rn(mx == -INFINITY ? 0.0f : acc / L);
-  if (p.lse && tid == 0) p.lse[orow] = (mx == -INFINITY) ? -INFINITY : (mx - kLift + log2f(L)) * 0.69314718055994530942f;
+      for (int k = 0; k < PARTS; ++k) {
+        const float f = exp2f(part_m[k] - M);
+        L += f * part_l[k];
+        acc += f * part_o[k][ch];
+      }
+    }
+  }
+  p.o[orow * D + ch] = __float2bfloat16_rn(M == -INFINITY ? 0.0f : acc / L);
+  if (p.lse && ch == 0) p.lse[orow] = (M == -INFINITY) ? -INFINITY : (M - kLift + log2f(L)) * 0.69314718055994530942f;
 }
 
-template <int D>
+template <int D, int NB>
 cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t st) {
-  const size_t smem = sizeof(Shared<D>) + (static_cast<size_t>(a.B) + 1) * sizeof(int);
-  cudaError_t e = ensure_dynamic_smem<decode_kernel<D>>(smem);
+  const size_t smem = static_cast<size_t>(kWarps) * stages(NB) * stage_bytes(D) +
+                      (a.idx ? 0 : (static_cast<size_t>(a.B) + 1) * sizeof(int));
+  cudaError_t e = ensure_dynamic_smem<decode_kernel<D, NB>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(decode_kernel<D>, dim3(a.num_ctas), dim3(kThreads), smem, st, a);
+  e = launch_dependent(decode_kernel<D, NB>, dim3(a.num_ctas), dim3(kThreads), smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(combine_kernel<D>, dim3(a.B * a.Hq), dim3(D), 0, st, a);
+  // records a row: the ranges over the rows, on average; over one round of eight they are shared out
+  if (a.num_ctas > 8 * a.B * a.Hkv) return launch_dependent(combine_kernel<D, 4>, dim3(a.B * a.Hq), dim3(4 * D), 0, st, a);
+  return launch_dependent(combine_kernel<D, 1>, dim3(a.B * a.Hq), dim3(D), 0, st, a);
 }
 
 }  // namespace qdecode
 
-int quant_decode_ctas(int num_sms) { return qdecode::kCtasPerSm * num_sms; }
+int quant_decode_ctas(int num_sms, int group) { return qdecode::ctas_per_sm(group > 8 ? 2 : 1) * num_sms; }
 
 cudaError_t launch_attn_decode_quant(const QuantDecodeArgs& a, int d, cudaStream_t st) {
-  return d == 64 ? qdecode::launch<64>(a, st) : qdecode::launch<128>(a, st);
+  if (a.Hq / a.Hkv > 8) return d == 64 ? qdecode::launch<64, 2>(a, st) : qdecode::launch<128, 2>(a, st);
+  return d == 64 ? qdecode::launch<64, 1>(a, st) : qdecode::launch<128, 1>(a, st);
 }
 
 }  // namespace bsa

@@ -192,7 +192,7 @@ struct QuantDecodeArgs {
   float* lse;
   uint32_t* status;
 };
-int quant_decode_ctas(int num_sms);
+int quant_decode_ctas(int num_sms, int group);
 cudaError_t launch_attn_decode_quant(const QuantDecodeArgs& a, int d, cudaStream_t st);
 
 // topk_lens.cu
