@@ -963,7 +963,7 @@ bsa_status_t bsa_paged_append_quant(const bsa_shape_t* s, const void* k_new, con
   if (!k_new || !v_new || !seq_lens || !aligned16(k_new) || !aligned16(v_new)) return BSA_ERR_INVALID_ARG;
   if (k_pool == v_pool || k_exp == v_exp || (pooled_k && !aligned16(pooled_k))) return BSA_ERR_INVALID_ARG;
   if (s->dtype != BSA_BF16) return BSA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(s->B) * s->Hkv * ((s->Nq + 62) / 64 + 1) >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->B) * s->Hkv * ((s->Nq + 62ll) / 64 + 1) >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
   QuantCacheArgs a{};
   if ((st = device_state(&a.status, nullptr)) != BSA_OK) return st;
   a.B = s->B;
@@ -991,7 +991,7 @@ bsa_status_t bsa_paged_read_quant(const bsa_shape_t* s, const void* k_pool, cons
   bsa_status_t st = quant_cache_checks(s, k_pool, v_pool, k_exp, v_exp, num_pages, block_table, table_stride);
   if (st != BSA_OK) return st;
   if (!seq_lens || (!k_out && !v_out) || !aligned16(k_out) || !aligned16(v_out)) return BSA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(s->B) * s->Hkv * s->Nq * (s->d / 8) >= (1ll << 38)) return BSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->B) * s->Hkv * ((s->Nq + 63ll) / 64) >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
   QuantCacheArgs a{};
   if ((st = device_state(&a.status, nullptr)) != BSA_OK) return st;
   a.B = s->B;

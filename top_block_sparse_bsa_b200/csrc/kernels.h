@@ -167,8 +167,7 @@ struct QuantCacheArgs {
   float* pooled;
   void *k_out, *v_out;
   uint32_t* status;
-  int touched;                 // set by the launchers
-  int64_t total;
+  int touched;                 // set by the launchers: 64-token pieces of a sequence
 };
 cudaError_t launch_quant_append(QuantCacheArgs a, cudaStream_t st);
 cudaError_t launch_quant_read(QuantCacheArgs a, bool bf16, cudaStream_t st);

@@ -46,6 +46,48 @@ __device__ __forceinline__ void decode8(uint2 w, float scale, float (&v)[8]) {
   }
 }
 
+// Largest of the lane group's 16-bit magnitudes (bf16 bits without the sign
+// order as whole numbers; infinity and NaN come out at 0x7F80 and above).
+template <int GS>
+__device__ __forceinline__ uint32_t group_max(uint32_t m, uint32_t group_mask) {
+#pragma unroll
+  for (int o = GS / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(group_mask, m, o));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// The codes of a lane's eight bf16 values and the row's exponent byte.
+template <int GS>
+__device__ __forceinline__ uint2 quantise_row(uint4 x, uint32_t group_mask, uint32_t& e) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                        __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  m = group_max<GS>(m, group_mask);
+  const bool broken = m >= 0x7F80u;      // the same for the whole row
+  if (broken) {
+    m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+      m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    }
+    m = group_max<GS>(m, group_mask);
+  }
+  e = exponent_byte(__uint_as_float(m << 16));
+  const float inv = two_to(254u - e);
+  uint32_t code[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
+    uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(lo * inv, hi * inv), __NV_SATFINITE, __NV_E4M3);
+    if (broken) {
+      if (!(fabsf(lo) < INFINITY)) two = (two & 0xFF00u) | 0x7Fu;
+      if (!(fabsf(hi) < INFINITY)) two = (two & 0x00FFu) | 0x7F00u;
+    }
+    code[i >> 1] |= two << ((i & 1) * 16);
+  }
+  return make_uint2(code[0], code[1]);
+}
+
 // One CTA per (sequence, KV head, touched block): the block's new tokens are
 // quantised row by row (GS lanes a row, eight channels a lane; keys and values
 // alternate), and if the append completes the block its mean key is summed
@@ -56,8 +98,8 @@ template <int GS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const QuantCacheArgs p) {
   griddep_wait();
   extern __shared__ uint4 smem_q[];
-  uint8_t* codes = reinterpret_cast<uint8_t*>(smem_q);       // [64][d]
-  uint8_t* exps = codes + 64 * p.d;                            // [64]
+  uint8_t* codes = reinterpret_cast<uint8_t*>(smem_q);          // [64][d]
+  float* scales = reinterpret_cast<float*>(codes + 64 * p.d);    // [64]
   const int j = blockIdx.x % p.touched;
   const int bg = blockIdx.x / p.touched;
   const int b = bg / p.Hkv, g = bg - b * p.Hkv;
@@ -84,49 +126,32 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const QuantCacheArgs p
   const bool on = 8 * l < p.d;
   // the lanes of this row's group: the groups of a warp may leave the loop at different rows
   const uint32_t group_mask = (GS == 32 ? 0xffffffffu : ((1u << (GS & 31)) - 1u)) << (threadIdx.x % 32 / GS * GS);
-  for (int r0 = grp; r0 < 2 * rows; r0 += kThreads / GS * 4) {
-    uint4 x[4];
+  constexpr int kGroups = kThreads / GS, kFlight = 4;
+  const __nv_bfloat16* k_src = static_cast<const __nv_bfloat16*>(p.k_new) + src0 * p.d + 8 * l;
+  const __nv_bfloat16* v_src = static_cast<const __nv_bfloat16*>(p.v_new) + src0 * p.d + 8 * l;
+  uint8_t* k_dst = p.k_pool + (page_row + o0) * p.d + 8 * l;
+  uint8_t* v_dst = p.v_pool + (page_row + o0) * p.d + 8 * l;
+  for (int r0 = grp; r0 < 2 * rows; r0 += kGroups * kFlight) {
+    uint4 x[kFlight];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = r0 + u * (kThreads / GS);
+    for (int u = 0; u < kFlight; ++u) {
+      const int r = r0 + u * kGroups;
       x[u] = make_uint4(0, 0, 0, 0);
       if (r < 2 * rows && on)
-        x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(r & 1 ? p.v_new : p.k_new) +
-                                                    (src0 + (r >> 1)) * p.d + 8 * l));
+        x[u] = __ldg(reinterpret_cast<const uint4*>((r & 1 ? v_src : k_src) + (r >> 1) * p.d));
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = r0 + u * (kThreads / GS);
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float v[8], m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.0f);
-#pragma unroll
-      for (int o = GS / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(group_mask, m, o));
-      const uint32_t e = exponent_byte(m);
-      const float inv = two_to(254u - e);
-      uint32_t code[2] = {0u, 0u};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE,
-                                                __NV_E4M3);
-        if (!(fabsf(v[2 * i]) < INFINITY)) two = (two & 0xFF00u) | 0x7Fu;
-        if (!(fabsf(v[2 * i + 1]) < INFINITY)) two = (two & 0x00FFu) | 0x7F00u;
-        code[i >> 1] |= two << ((i & 1) * 16);
-      }
-      if (r < 2 * rows && on) {
-        const int o = o0 + (r >> 1);
-        uint8_t* pool = r & 1 ? p.v_pool : p.k_pool;
-        *reinterpret_cast<uint2*>(pool + (page_row + o) * p.d + 8 * l) = make_uint2(code[0], code[1]);
-        if (l == 0) (r & 1 ? p.v_exp : p.k_exp)[page_row + o] = static_cast<uint8_t>(e);
+    for (int u = 0; u < kFlight; ++u) {
+      const int r = r0 + u * kGroups, t = r >> 1;
+      if (r >= 2 * rows) break;
+      uint32_t e;
+      const uint2 code = quantise_row<GS>(x[u], group_mask, e);
+      if (on) {
+        *reinterpret_cast<uint2*>((r & 1 ? v_dst : k_dst) + t * p.d) = code;
+        if (l == 0) (r & 1 ? p.v_exp : p.k_exp)[page_row + o0 + t] = static_cast<uint8_t>(e);
         if (complete && !(r & 1)) {
-          *reinterpret_cast<uint2*>(codes + o * p.d + 8 * l) = make_uint2(code[0], code[1]);
-          if (l == 0) exps[o] = static_cast<uint8_t>(e);
+          *reinterpret_cast<uint2*>(codes + (o0 + t) * p.d + 8 * l) = code;
+          if (l == 0) scales[o0 + t] = two_to(e);
         }
       }
     }
@@ -135,76 +160,112 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const QuantCacheArgs p
   // the tokens that lay in this block before (positions [0, o0) of it)
   for (int t = threadIdx.x; t < o0 * (p.d / 8); t += kThreads)
     reinterpret_cast<uint2*>(codes)[t] = reinterpret_cast<const uint2*>(p.k_pool + page_row * p.d)[t];
-  for (int t = threadIdx.x; t < o0; t += kThreads) exps[t] = p.k_exp[page_row + t];
+  for (int t = threadIdx.x; t < o0; t += kThreads) scales[t] = two_to(p.k_exp[page_row + t]);
   __syncthreads();
-  for (int ch = threadIdx.x; ch < p.d; ch += kThreads) {
-    float sum = 0.0f;
+  // four channels a thread: a product is exact, so the fused form rounds each sum once, as the pooling does
+  const int ch = 4 * threadIdx.x;
+  if (ch >= p.d) return;
+  float sum[4] = {};
 #pragma unroll 16
-    for (int t = 0; t < 64; ++t) {
-      const __half h = __half(__nv_cvt_fp8_to_halfraw(codes[t * p.d + ch], __NV_E4M3));
-      sum = __fadd_rn(sum, __fmul_rn(__half2float(h), two_to(exps[t])));
-    }
-    p.pooled[(static_cast<int64_t>(bg) * p.table_stride + blk) * p.d + ch] = __fdiv_rn(sum, 64.0f);
+  for (int t = 0; t < 64; ++t) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + t * p.d + ch);
+    const float scale = scales[t];
+    const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
+    const float2 c =
+        __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3)));
+    sum[0] = fmaf(a.x, scale, sum[0]);
+    sum[1] = fmaf(a.y, scale, sum[1]);
+    sum[2] = fmaf(c.x, scale, sum[2]);
+    sum[3] = fmaf(c.y, scale, sum[3]);
   }
+  *reinterpret_cast<float4*>(p.pooled + (static_cast<int64_t>(bg) * p.table_stride + blk) * p.d + ch) =
+      make_float4(__fdiv_rn(sum[0], 64.0f), __fdiv_rn(sum[1], 64.0f), __fdiv_rn(sum[2], 64.0f),
+                  __fdiv_rn(sum[3], 64.0f));
 }
 
 // Tokens starts[b] + t of every sequence and head, t < T and below the
 // sequence's length, as bf16 (exact) or fp32 rows; other output rows are left
-// as they were.  One thread per eight channels.
-template <typename T>
+// as they were.  One CTA per 64 output rows of a (sequence, head); GS lanes a
+// row, eight channels a lane, a lane's keys and values of four rows in flight.
+template <typename T, int GS>
 __global__ void __launch_bounds__(kThreads) read_kernel(const QuantCacheArgs p) {
   griddep_wait();
-  const int pieces = p.d / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= p.total) return;
-  const int piece = static_cast<int>(i % pieces);
-  const int64_t row = i / pieces;                 // (b * Hkv + g) * T + t
-  const int t = static_cast<int>(row % p.T);
-  const int64_t bg = row / p.T;
-  const int b = static_cast<int>(bg / p.Hkv), g = static_cast<int>(bg - static_cast<int64_t>(b) * p.Hkv);
-  const int64_t pos = (p.starts ? p.starts[b] : 0) + static_cast<int64_t>(t);
-  if (pos >= p.seq_lens[b]) return;
-  const int64_t blk = pos >> 6;
-  const int page = (pos >= 0 && blk < p.table_stride) ? __ldg(p.table + static_cast<int64_t>(b) * p.table_stride + blk) : -1;
-  if (page < 0 || page >= p.num_pages) {
-    atomicOr(p.status, BSA_DEV_BAD_INDEX);
-    return;
-  }
-  const int64_t src = (static_cast<int64_t>(page) * p.Hkv + g) * 64 + (pos & 63);
+  constexpr int kGroups = kThreads / GS, kFlight = 4;
+  const int tile = blockIdx.x % p.touched;
+  const int bg = blockIdx.x / p.touched;
+  const int b = bg / p.Hkv, g = bg - b * p.Hkv;
+  const int64_t start = p.starts ? p.starts[b] : 0;
+  const int t_end = static_cast<int>(min(min(static_cast<int64_t>(p.T), p.seq_lens[b] - start), static_cast<int64_t>(tile) * 64 + 64));
+  const int l = threadIdx.x % GS, grp = threadIdx.x / GS;
+  if (8 * l >= p.d) return;
+  for (int t0 = tile * 64 + grp; t0 < t_end; t0 += kGroups * kFlight) {
+    uint2 code[2][kFlight];
+    uint32_t e[2][kFlight];
+    bool ok[kFlight];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    T* out = static_cast<T*>(kv ? p.v_out : p.k_out);
-    if (out == nullptr) continue;
-    float v[8];
-    decode8(__ldg(reinterpret_cast<const uint2*>((kv ? p.v_pool : p.k_pool) + src * p.d + 8 * piece)),
-            two_to((kv ? p.v_exp : p.k_exp)[src]), v);
-    T* dst = out + row * p.d + 8 * piece;
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    } else {
-      reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int u = 0; u < kFlight; ++u) {
+      const int t = t0 + u * kGroups;
+      const int64_t pos = start + t, blk = pos >> 6;
+      int page = -1;
+      ok[u] = false;
+      if (t < t_end) {
+        if (pos >= 0 && blk < p.table_stride) page = __ldg(p.table + static_cast<int64_t>(b) * p.table_stride + blk);
+        ok[u] = page >= 0 && page < p.num_pages;
+        if (!ok[u]) atomicOr(p.status, BSA_DEV_BAD_INDEX);
+      }
+      const int64_t src = (static_cast<int64_t>(page) * p.Hkv + g) * 64 + (pos & 63);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        code[kv][u] = make_uint2(0u, 0u);
+        e[kv][u] = 0u;
+        if (ok[u] && (kv ? p.v_out : p.k_out) != nullptr) {
+          code[kv][u] = __ldg(reinterpret_cast<const uint2*>((kv ? p.v_pool : p.k_pool) + src * p.d + 8 * l));
+          e[kv][u] = __ldg((kv ? p.v_exp : p.k_exp) + src);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        T* out = static_cast<T*>(kv ? p.v_out : p.k_out);
+        if (!ok[u] || out == nullptr) continue;
+        float v[8];
+        decode8(code[kv][u], two_to(e[kv][u]), v);
+        T* dst = out + (static_cast<int64_t>(bg) * p.T + t0 + u * kGroups) * p.d + 8 * l;
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        } else {
+          reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
     }
   }
+}
+
+template <typename T>
+cudaError_t launch_read(const QuantCacheArgs& a, unsigned grid, cudaStream_t st) {
+  auto kernel = a.d <= 64 ? read_kernel<T, 8> : (a.d <= 128 ? read_kernel<T, 16> : read_kernel<T, 32>);
+  return launch_dependent(kernel, dim3(grid), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace qcache
 
 cudaError_t launch_quant_append(QuantCacheArgs a, cudaStream_t st) {
   // an append of T tokens touches at most this many blocks of a sequence
-  a.touched = (a.T + 62) / 64 + 1;
+  a.touched = static_cast<int>((a.T + 62ll) / 64 + 1);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hkv * a.touched);
-  const size_t smem = 64 * static_cast<size_t>(a.d) + 64;
+  const size_t smem = 64 * (static_cast<size_t>(a.d) + sizeof(float));
   auto kernel = a.d <= 64 ? qcache::append_kernel<8> : (a.d <= 128 ? qcache::append_kernel<16> : qcache::append_kernel<32>);
   return launch_dependent(kernel, dim3(grid), dim3(qcache::kThreads), smem, st, a);
 }
 
 cudaError_t launch_quant_read(QuantCacheArgs a, bool bf16, cudaStream_t st) {
-  a.total = static_cast<int64_t>(a.B) * a.Hkv * a.T * (a.d / 8);
-  const unsigned grid = static_cast<unsigned>((a.total + qcache::kThreads - 1) / qcache::kThreads);
-  return launch_dependent(bf16 ? qcache::read_kernel<__nv_bfloat16> : qcache::read_kernel<float>, dim3(grid),
-                          dim3(qcache::kThreads), 0, st, a);
+  a.touched = static_cast<int>((a.T + 63ll) / 64);
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hkv * a.touched);
+  return bf16 ? qcache::launch_read<__nv_bfloat16>(a, grid, st) : qcache::launch_read<float>(a, grid, st);
 }
 
 }  // namespace bsa
