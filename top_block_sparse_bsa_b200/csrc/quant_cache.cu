@@ -46,60 +46,68 @@ __device__ __forceinline__ void decode8(uint2 w, float scale, float (&v)[8]) {
   }
 }
 
-// Largest of the lane group's 16-bit magnitudes (bf16 bits without the sign
-// order as whole numbers; infinity and NaN come out at 0x7F80 and above).
+// Largest magnitude of two or three values; NaN if one is NaN.
+__device__ __forceinline__ float amax2(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return d;
+}
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
 template <int GS>
-__device__ __forceinline__ uint32_t group_max(uint32_t m, uint32_t group_mask) {
+__device__ __forceinline__ float group_amax(float m, uint32_t group_mask) {
 #pragma unroll
-  for (int o = GS / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(group_mask, m, o));
-  return max(m & 0xFFFFu, m >> 16);
+  for (int o = GS / 2; o; o >>= 1) m = amax2(m, __shfl_xor_sync(group_mask, m, o));
+  return m;
 }
 
 // The codes of a lane's eight bf16 values and the row's exponent byte.
 template <int GS>
 __device__ __forceinline__ uint2 quantise_row(uint4 x, uint32_t group_mask, uint32_t& e) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                        __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-  m = group_max<GS>(m, group_mask);
-  const bool broken = m >= 0x7F80u;      // the same for the whole row
-  if (broken) {
-    m = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-      m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-    }
-    m = group_max<GS>(m, group_mask);
-  }
-  e = exponent_byte(__uint_as_float(m << 16));
-  const float inv = two_to(254u - e);
-  uint32_t code[2] = {0u, 0u};
+  float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
-    uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(lo * inv, hi * inv), __NV_SATFINITE, __NV_E4M3);
-    if (broken) {
-      if (!(fabsf(lo) < INFINITY)) two = (two & 0xFF00u) | 0x7Fu;
-      if (!(fabsf(hi) < INFINITY)) two = (two & 0x00FFu) | 0x7F00u;
-    }
-    code[i >> 1] |= two << ((i & 1) * 16);
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  return make_uint2(code[0], code[1]);
+  float m = group_amax<GS>(amax2(amax3(amax3(v[0], v[1], v[2]), v[3], v[4]), amax3(v[5], v[6], v[7])), group_mask);
+  const bool broken = !(m < INFINITY);      // the same for the whole row
+  if (broken) {
+    m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.0f);
+    m = group_amax<GS>(m, group_mask);
+  }
+  e = exponent_byte(m);
+  const float inv = two_to(254u - e);
+  uint32_t code[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    code[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    if (broken) {
+      if (!(fabsf(v[2 * i]) < INFINITY)) code[i] = (code[i] & 0xFF00u) | 0x7Fu;
+      if (!(fabsf(v[2 * i + 1]) < INFINITY)) code[i] = (code[i] & 0x00FFu) | 0x7F00u;
+    }
+  }
+  return make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
 }
 
 // One CTA per (sequence, KV head, touched block): the block's new tokens are
-// quantised row by row (GS lanes a row, eight channels a lane; keys and values
-// alternate), and if the append completes the block its mean key is summed
+// quantised row by row (GS lanes a row, eight channels a lane, keys and values
+// of two tokens in flight), and if the append completes the block its mean key is summed
 // from the codes, tokens ascending, fp32, one division -- from shared memory,
 // which also takes the tokens that lay in the block before.  One launch, no
 // block waits for another.
 template <int GS>
-__global__ void __launch_bounds__(kThreads) append_kernel(const QuantCacheArgs p) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(const QuantCacheArgs p) {
   griddep_wait();
   extern __shared__ uint4 smem_q[];
   uint8_t* codes = reinterpret_cast<uint8_t*>(smem_q);          // [64][d]
-  float* scales = reinterpret_cast<float*>(codes + 64 * p.d);    // [64]
+  __shared__ uint8_t exps[2][64];
   const int j = blockIdx.x % p.touched;
   const int bg = blockIdx.x / p.touched;
   const int b = bg / p.Hkv, g = bg - b * p.Hkv;
@@ -113,12 +121,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const QuantCacheArgs p
   const int64_t blk = (L >> 6) + j;
   const int64_t first = max(L, blk * 64), end = min(L + n, blk * 64 + 64);   // positions written here
   if (first >= end) return;
-  const int page = blk < p.table_stride ? p.table[static_cast<int64_t>(b) * p.table_stride + blk] : -1;
-  if (page < 0 || page >= p.num_pages) {
-    if (threadIdx.x == 0) atomicOr(p.status, BSA_DEV_BAD_INDEX);
-    return;
-  }
-  const int64_t page_row = (static_cast<int64_t>(page) * p.Hkv + g) * 64;
   const bool complete = p.pooled != nullptr && L + n >= blk * 64 + 64;
   const int o0 = static_cast<int>(first & 63), rows = static_cast<int>(end - first);
   const int64_t src0 = static_cast<int64_t>(bg) * p.T + (first - L);
@@ -126,61 +128,72 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const QuantCacheArgs p
   const bool on = 8 * l < p.d;
   // the lanes of this row's group: the groups of a warp may leave the loop at different rows
   const uint32_t group_mask = (GS == 32 ? 0xffffffffu : ((1u << (GS & 31)) - 1u)) << (threadIdx.x % 32 / GS * GS);
-  constexpr int kGroups = kThreads / GS, kFlight = 4;
-  const __nv_bfloat16* k_src = static_cast<const __nv_bfloat16*>(p.k_new) + src0 * p.d + 8 * l;
-  const __nv_bfloat16* v_src = static_cast<const __nv_bfloat16*>(p.v_new) + src0 * p.d + 8 * l;
-  uint8_t* k_dst = p.k_pool + (page_row + o0) * p.d + 8 * l;
-  uint8_t* v_dst = p.v_pool + (page_row + o0) * p.d + 8 * l;
-  for (int r0 = grp; r0 < 2 * rows; r0 += kGroups * kFlight) {
-    uint4 x[kFlight];
+  constexpr int kGroups = kThreads / GS, kFlight = 2;
+  const __nv_bfloat16* src[2] = {static_cast<const __nv_bfloat16*>(p.k_new) + src0 * p.d + 8 * l,
+                                 static_cast<const __nv_bfloat16*>(p.v_new) + src0 * p.d + 8 * l};
+  uint4 x[kFlight][2];
+  auto load = [&](int t0) {
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
-      const int r = r0 + u * kGroups;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (r < 2 * rows && on)
-        x[u] = __ldg(reinterpret_cast<const uint4*>((r & 1 ? v_src : k_src) + (r >> 1) * p.d));
+      const int t = t0 + u * kGroups;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        x[u][kv] = make_uint4(0, 0, 0, 0);
+        if (t < rows && on) x[u][kv] = __ldg(reinterpret_cast<const uint4*>(src[kv] + t * p.d));
+      }
     }
+  };
+  load(grp);       // the first rows are on their way while the page is looked up
+  const int page = blk < p.table_stride ? p.table[static_cast<int64_t>(b) * p.table_stride + blk] : -1;
+  if (page < 0 || page >= p.num_pages) {
+    if (threadIdx.x == 0) atomicOr(p.status, BSA_DEV_BAD_INDEX);
+    return;
+  }
+  const int64_t page_row = (static_cast<int64_t>(page) * p.Hkv + g) * 64;
+  uint8_t* dst[2] = {p.k_pool + (page_row + o0) * p.d + 8 * l, p.v_pool + (page_row + o0) * p.d + 8 * l};
+  for (int t0 = grp; t0 < rows; t0 += kGroups * kFlight) {
+    if (t0 != grp) load(t0);
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
-      const int r = r0 + u * kGroups, t = r >> 1;
-      if (r >= 2 * rows) break;
-      uint32_t e;
-      const uint2 code = quantise_row<GS>(x[u], group_mask, e);
-      if (on) {
-        *reinterpret_cast<uint2*>((r & 1 ? v_dst : k_dst) + t * p.d) = code;
-        if (l == 0) (r & 1 ? p.v_exp : p.k_exp)[page_row + o0 + t] = static_cast<uint8_t>(e);
-        if (complete && !(r & 1)) {
-          *reinterpret_cast<uint2*>(codes + (o0 + t) * p.d + 8 * l) = code;
-          if (l == 0) scales[o0 + t] = two_to(e);
-        }
+      const int t = t0 + u * kGroups;
+      if (t >= rows) break;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint32_t e;
+        const uint2 code = quantise_row<GS>(x[u][kv], group_mask, e);
+        if (!on) continue;
+        *reinterpret_cast<uint2*>(dst[kv] + t * p.d) = code;
+        if (l == 0) exps[kv][o0 + t] = static_cast<uint8_t>(e);
+        if (kv == 0 && complete) *reinterpret_cast<uint2*>(codes + (o0 + t) * p.d + 8 * l) = code;
       }
     }
   }
-  if (!complete) return;
-  // the tokens that lay in this block before (positions [0, o0) of it)
-  for (int t = threadIdx.x; t < o0 * (p.d / 8); t += kThreads)
-    reinterpret_cast<uint2*>(codes)[t] = reinterpret_cast<const uint2*>(p.k_pool + page_row * p.d)[t];
-  for (int t = threadIdx.x; t < o0; t += kThreads) scales[t] = two_to(p.k_exp[page_row + t]);
-  __syncthreads();
-  // four channels a thread: a product is exact, so the fused form rounds each sum once, as the pooling does
-  const int ch = 4 * threadIdx.x;
-  if (ch >= p.d) return;
-  float sum[4] = {};
-#pragma unroll 16
-  for (int t = 0; t < 64; ++t) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + t * p.d + ch);
-    const float scale = scales[t];
-    const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
-    const float2 c =
-        __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3)));
-    sum[0] = fmaf(a.x, scale, sum[0]);
-    sum[1] = fmaf(a.y, scale, sum[1]);
-    sum[2] = fmaf(c.x, scale, sum[2]);
-    sum[3] = fmaf(c.y, scale, sum[3]);
+  if (complete) {   // the tokens that lay in this block before (positions [0, o0) of it)
+    for (int t = threadIdx.x; t < o0 * (p.d / 8); t += kThreads)
+      reinterpret_cast<uint2*>(codes)[t] = reinterpret_cast<const uint2*>(p.k_pool + page_row * p.d)[t];
+    for (int t = threadIdx.x; t < o0; t += kThreads) exps[0][t] = p.k_exp[page_row + t];
   }
-  *reinterpret_cast<float4*>(p.pooled + (static_cast<int64_t>(bg) * p.table_stride + blk) * p.d + ch) =
-      make_float4(__fdiv_rn(sum[0], 64.0f), __fdiv_rn(sum[1], 64.0f), __fdiv_rn(sum[2], 64.0f),
-                  __fdiv_rn(sum[3], 64.0f));
+  __syncthreads();
+  // the new rows' exponents, together
+  if (threadIdx.x >= 128) {
+    const int kv = (threadIdx.x >> 6) & 1, o = threadIdx.x & 63;
+    if (o >= o0 && o < o0 + rows) (kv ? p.v_exp : p.k_exp)[page_row + o] = exps[kv][o];
+  }
+  if (!complete) return;
+  // two channels a thread: a product is exact, so the fused form rounds each sum once, as the pooling does
+  for (int ch = 2 * threadIdx.x; ch < p.d; ch += 2 * kThreads) {
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 16
+    for (int t = 0; t < 64; ++t) {
+      const __nv_fp8x2_storage_t two = *reinterpret_cast<const __nv_fp8x2_storage_t*>(codes + t * p.d + ch);
+      const float scale = two_to(exps[0][t]);
+      const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+      s0 = fmaf(a.x, scale, s0);
+      s1 = fmaf(a.y, scale, s1);
+    }
+    *reinterpret_cast<float2*>(p.pooled + (static_cast<int64_t>(bg) * p.table_stride + blk) * p.d + ch) =
+        make_float2(__fdiv_rn(s0, 64.0f), __fdiv_rn(s1, 64.0f));
+  }
 }
 
 // Tokens starts[b] + t of every sequence and head, t < T and below the
@@ -257,7 +270,7 @@ cudaError_t launch_quant_append(QuantCacheArgs a, cudaStream_t st) {
   // an append of T tokens touches at most this many blocks of a sequence
   a.touched = static_cast<int>((a.T + 62ll) / 64 + 1);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hkv * a.touched);
-  const size_t smem = 64 * (static_cast<size_t>(a.d) + sizeof(float));
+  const size_t smem = 64 * static_cast<size_t>(a.d);
   auto kernel = a.d <= 64 ? qcache::append_kernel<8> : (a.d <= 128 ? qcache::append_kernel<16> : qcache::append_kernel<32>);
   return launch_dependent(kernel, dim3(grid), dim3(qcache::kThreads), smem, st, a);
 }
