@@ -574,8 +574,8 @@ bsa_status_t bsa_sparse_attn_decode_quant(const bsa_shape_t* shape, const void* 
  * Cite: SAS page, 推理 paragraph and 核心模块 3; 稀疏注意力 tutorial §5.
  * scores [rows, ncols] fp32; row r belongs to sequence r / rows_per_len, which
  * holds lens[r / rows_per_len] tokens = n blocks of `block` (the last may be
- * partial).  Candidates j < n-1; block n-1 always kept; columns from n-1 on are
- * not read.  Order and outputs as bsa_topk_select (idx_stride >= kb + 1); a
+ * partial).  Candidates j < n-1; block n-1 always kept; columns from n-1 on
+ * do not count, whatever they hold.  Order and outputs as bsa_topk_select (idx_stride >= kb + 1); a
  * sequence without tokens keeps nothing.  A length of more than ncols blocks is
  * taken as ncols blocks and flagged (BSA_DEV_BAD_INDEX).  rows must be a
  * multiple of rows_per_len.  Limits: ncols <= 8192.
