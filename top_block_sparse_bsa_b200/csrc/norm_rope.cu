@@ -31,22 +31,22 @@ namespace bsa {
 namespace nrope {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;   // rows a lane of the forward has in flight
+// rows a lane of the forward has in flight, and blocks an SM (32K tokens of 48 heads, us): bf16 4 rows x 4 blocks 144,
+// 4 x 3 142, 3 x 4 147, 2 x 5 145, 8 x 2 149, 6 x 3 155; fp32 3 x 3 252, 4 x 3 257, 4 x 4 280
+template <typename T>
+__host__ __device__ constexpr int fwd_rows() {
+  return sizeof(T) == 2 ? 4 : 3;
+}
+template <typename T>
+__host__ __device__ constexpr int fwd_ctas() {
+  return sizeof(T) == 2 ? 4 : 3;
+}
 constexpr int kBwdCtasPerSm = 2;
 
 enum { LAYOUT_NONE = 0, LAYOUT_HALF = 1, LAYOUT_PAIRS = 2 };
 
-// Four consecutive channels of a row.
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-  const float4 t = __ldg(reinterpret_cast<const float4*>(p));
-  v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
-  const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
-  v[0] = __uint_as_float(t.x << 16); v[1] = __uint_as_float(t.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(t.y << 16); v[3] = __uint_as_float(t.y & 0xFFFF0000u);
-}
-// The same, kept as loaded: a bf16 piece waits for its turn in two registers.
+// Four consecutive channels of a row, kept as loaded: a bf16 piece waits for
+// its turn in two registers.  pairs() gives them as two packed fp32 pairs.
 template <typename T>
 struct Raw;
 template <>
@@ -54,24 +54,35 @@ struct Raw<float> {
   float4 v;
   __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
-  __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
+  __device__ __forceinline__ void pairs(uint64_t& lo, uint64_t& hi) const {
+    lo = f2_pack(v.x, v.y);
+    hi = f2_pack(v.z, v.w);
+  }
 };
 template <>
 struct Raw<__nv_bfloat16> {
   uint2 v;
   __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
-  __device__ __forceinline__ void get(float (&x)[4]) const {
-    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = v; }
+  __device__ __forceinline__ void pairs(uint64_t& lo, uint64_t& hi) const {
+    lo = f2_pack(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+    hi = f2_pack(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
   }
 };
-__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
 // The one rounding of the operator: fp32 results to the output's type.
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+__device__ __forceinline__ void store_pairs(float* p, uint64_t lo, uint64_t hi) {
+  float4 v;
+  f2_unpack(lo, v.x, v.y);
+  f2_unpack(hi, v.z, v.w);
+  *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, uint64_t lo, uint64_t hi) {
+  float a, b, c, d;
+  f2_unpack(lo, a, b);
+  f2_unpack(hi, c, d);
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
 // The channels of one lane: pieces [a, a+4) and [b, b+4); `on`: they exist;
@@ -93,6 +104,18 @@ __device__ __forceinline__ Lane lane_channels(int l, int d, int rot) {
   m.on = 8 * l < d;
   m.rotated = LAYOUT != LAYOUT_NONE && 8 * l < rot;
   return m;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_weight(const T* __restrict__ weight, const Lane& m, float (&w)[8]) {
+  Raw<T> a, b;
+  a.load(weight + m.a);
+  b.load(weight + m.b);
+  uint64_t x[4];
+  a.pairs(x[0], x[1]);
+  b.pairs(x[2], x[3]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f2_unpack(x[k], w[2 * k], w[2 * k + 1]);
 }
 
 // Frequencies as fractions of a turn, 2^64 to the turn, in shared memory: one
@@ -119,26 +142,32 @@ __device__ __forceinline__ void angles(const unsigned long long* __restrict__ f,
     s[i] = sn * scale;
   }
 }
-// (a, b) turned by (c, s); the half layout pairs a[i] with b[i], the other one
-// neighbours inside each piece.
+// A lane's eight channels as packed pairs X[0..3] = (a0,a1) (a2,a3) (b0,b1)
+// (b2,b3).  A rotation (with factors on the channels) is P X + Q X', where X'
+// is the pair that holds X's partners: X[k ^ 2] in the half layout, X itself
+// with its two halves exchanged in the other.
 template <int LAYOUT>
-__device__ __forceinline__ void rotate(float (&a)[4], float (&b)[4], const float (&c)[4], const float (&s)[4]) {
-  if (LAYOUT == LAYOUT_HALF) {
+__device__ __forceinline__ uint64_t partner(const uint64_t (&x)[4], int k) {
+  if (LAYOUT == LAYOUT_HALF) return x[k ^ 2];
+  float lo, hi;
+  f2_unpack(x[k], lo, hi);
+  return f2_pack(hi, lo);
+}
+// P and Q of the turn by (c, s) of channels whose factors are w: y = turn(w x).
+template <int LAYOUT>
+__device__ __forceinline__ void turn_factors(const float (&c)[4], const float (&s)[4], const float (&w)[8],
+                                             uint64_t (&P)[4], uint64_t (&Q)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = a[i], y = b[i];
-      a[i] = x * c[i] - y * s[i];
-      b[i] = x * s[i] + y * c[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float x = a[2 * i], y = a[2 * i + 1];
-      a[2 * i] = x * c[i] - y * s[i];
-      a[2 * i + 1] = x * s[i] + y * c[i];
-      x = b[2 * i], y = b[2 * i + 1];
-      b[2 * i] = x * c[2 + i] - y * s[2 + i];
-      b[2 * i + 1] = x * s[2 + i] + y * c[2 + i];
+  for (int k = 0; k < 4; ++k) {
+    const int i0 = 2 * k, i1 = 2 * k + 1;          // the pair's channels among the lane's eight
+    if (LAYOUT == LAYOUT_HALF) {
+      const int q = i0 & 3, o = i0 ^ 4;            // angles of the pair; partners o, o + 1
+      const float sign = k < 2 ? -1.0f : 1.0f;
+      P[k] = f2_pack(w[i0] * c[q], w[i1] * c[q + 1]);
+      Q[k] = f2_pack(sign * w[o] * s[q], sign * w[o + 1] * s[q + 1]);
+    } else {
+      P[k] = f2_pack(w[i0] * c[k], w[i1] * c[k]);
+      Q[k] = f2_pack(-w[i1] * s[k], w[i0] * s[k]);
     }
   }
 }
@@ -153,9 +182,9 @@ __device__ __forceinline__ float row_sum(float v) {
 // Work items: token tiles (kThreads/GS tokens, one per lane group) x runs of
 // head_run heads.
 template <typename T, int GS, int LAYOUT>
-__global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const NormRopeArgs p) {
+__global__ void __launch_bounds__(kThreads, fwd_ctas<T>()) fwd_kernel(const NormRopeArgs p) {
   griddep_wait();
-  constexpr int kTokens = kThreads / GS;
+  constexpr int kTokens = kThreads / GS, kUnroll = fwd_rows<T>();
   __shared__ unsigned long long freqs[kMaxPairs];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS;
   const Lane m = lane_channels<LAYOUT>(l, p.d, p.rot);
@@ -178,20 +207,33 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const NormRopeArgs p) 
     const int from = max(h_begin, lo), to = min(h_end, lo + heads);
     if (from >= to) continue;
     const T* weight = static_cast<const T*>(part == 0 ? p.q_weight : p.k_weight);
-    T* out = static_cast<T*>(part == 0 ? p.q : (part == 1 ? p.k : p.v));
+    const T* src = row0 + from * p.d;
+    const int64_t head_step = static_cast<int64_t>(p.N) * p.d;
+    T* dst = static_cast<T*>(part == 0 ? p.q : (part == 1 ? p.k : p.v)) +
+             (static_cast<int64_t>(b) * heads + (from - lo)) * head_step + static_cast<int64_t>(n) * p.d;
     const bool norm = part < 2 && weight != nullptr;
-    float wa[4], wb[4];
-    if (norm && m.on) {
-      load4(weight + m.a, wa);
-      load4(weight + m.b, wb);
+    const bool turned = LAYOUT != LAYOUT_NONE && part < 2 && m.rotated;
+    // the norm's weight rides in the rotation's factors; without a rotation P is the weight alone
+    uint64_t P[4], Q[4];
+    if (part < 2) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+      if (norm && m.on) load_weight(weight, m, w);
+      if (turned) {
+        turn_factors<LAYOUT>(c, s, w, P, Q);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) P[k] = f2_pack(w[2 * k], w[2 * k + 1]), Q[k] = 0;
+      }
     }
-    for (int h0 = from; h0 < to; h0 += kUnroll) {
+    for (int h0 = from; h0 < to; h0 += kUnroll, src += kUnroll * p.d, dst += kUnroll * head_step) {
       Raw<T> ra[kUnroll], rb[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (m.on && live && h0 + u < to) {
-          ra[u].load(row0 + (h0 + u) * p.d + m.a);
-          rb[u].load(row0 + (h0 + u) * p.d + m.b);
+          ra[u].load(src + u * p.d + m.a);
+          rb[u].load(src + u * p.d + m.b);
         } else {
           ra[u].zero();
           rb[u].zero();
@@ -199,25 +241,36 @@ __global__ void __launch_bounds__(kThreads, 4) fwd_kernel(const NormRopeArgs p) 
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        float xa[4], xb[4];
-        ra[u].get(xa);
-        rb[u].get(xb);
-        if (norm) {
-          float ss = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
-          const float r = rsqrtf(row_sum<GS>(ss) * p.inv_d + p.eps);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            xa[i] *= r * wa[i];
-            xb[i] *= r * wb[i];
+        const bool in = m.on && live && h0 + u < to;
+        T* to_row = dst + u * head_step;
+        if (part == 2) {
+          if (in) {
+            ra[u].store(to_row + m.a);
+            rb[u].store(to_row + m.b);
           }
+          continue;
         }
-        if (LAYOUT != LAYOUT_NONE && part < 2 && m.rotated) rotate<LAYOUT>(xa, xb, c, s);
-        if (m.on && live && h0 + u < to) {
-          T* dst = out + ((static_cast<int64_t>(b) * heads + (h0 + u - lo)) * p.N + n) * p.d;
-          store4(dst + m.a, xa);
-          store4(dst + m.b, xb);
+        uint64_t x[4], y[4];
+        ra[u].pairs(x[0], x[1]);
+        rb[u].pairs(x[2], x[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = f2_mul(P[k], x[k]);
+        if (turned) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = f2_fma(Q[k], partner<LAYOUT>(x, k), y[k]);
+        }
+        if (norm) {
+          const uint64_t s2 = f2_fma(x[3], x[3], f2_fma(x[2], x[2], f2_fma(x[1], x[1], f2_mul(x[0], x[0]))));
+          float lo2, hi2;
+          f2_unpack(s2, lo2, hi2);
+          const float r = rsqrtf(row_sum<GS>(lo2 + hi2) * p.inv_d + p.eps);
+          const uint64_t rr = f2_pack(r, r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = f2_mul(y[k], rr);
+        }
+        if (in) {
+          store_pairs(to_row + m.a, y[0], y[1]);
+          store_pairs(to_row + m.b, y[2], y[3]);
         }
       }
     }
@@ -258,11 +311,14 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
     const int h_begin = run * p.head_run, h_end = min(h_begin + p.head_run, H);
     const T* row0 = static_cast<const T*>(p.qkv) + tk * p.token_stride;
     T* drow0 = static_cast<T*>(p.d_qkv) + tk * p.d_token_stride;
-    float c[4], s[4];
+    uint64_t P[4] = {}, Q[4] = {};
     if (LAYOUT != LAYOUT_NONE && m.rotated && h_begin < p.Hq + p.Hkv) {
+      float c[4], s[4];
       angles(freqs + 4 * l, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = -s[i];
+      for (int i = 0; i < 4; ++i) s[i] = -s[i];       // turned back
+      const float ones[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+      turn_factors<LAYOUT>(c, s, ones, P, Q);
     }
     for (int part = 0; part < 3; ++part) {
       const int lo = part == 0 ? 0 : (part == 1 ? p.Hq : p.Hq + p.Hkv);
@@ -274,67 +330,78 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
                         (static_cast<int64_t>(b) * heads - lo) * head_step + static_cast<int64_t>(n) * p.d;
       const T* weight = static_cast<const T*>(part == 0 ? p.q_weight : p.k_weight);
       const bool nm = part < 2 && norm;
-      float wa[4] = {}, wb[4] = {}, dwa[4] = {}, dwb[4] = {};
+      const bool turned = LAYOUT != LAYOUT_NONE && part < 2 && m.rotated;
+      uint64_t W[4] = {}, dW[4] = {};
       if (nm && m.on) {
-        load4(weight + m.a, wa);
-        load4(weight + m.b, wb);
+        float w[8];
+        load_weight(weight, m, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) W[k] = f2_pack(w[2 * k], w[2 * k + 1]);
       }
       for (int h0 = from; h0 < to; h0 += kRows) {
-        Raw<float> ga_[kRows], gb_[kRows];
-        Raw<T> xa_[kRows], xb_[kRows];
+        Raw<float> ga[kRows], gb[kRows];
+        Raw<T> xa[kRows], xb[kRows];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          ga_[u].zero(), gb_[u].zero(), xa_[u].zero(), xb_[u].zero();
+          ga[u].zero(), gb[u].zero(), xa[u].zero(), xb[u].zero();
           if (m.on && live && h0 + u < to) {
             const float* src = dz + (h0 + u) * head_step;
-            ga_[u].load(src + m.a);
-            gb_[u].load(src + m.b);
+            ga[u].load(src + m.a);
+            gb[u].load(src + m.b);
             if (nm) {
-              xa_[u].load(row0 + (h0 + u) * p.d + m.a);
-              xb_[u].load(row0 + (h0 + u) * p.d + m.b);
+              xa[u].load(row0 + (h0 + u) * p.d + m.a);
+              xb[u].load(row0 + (h0 + u) * p.d + m.b);
             }
           }
         }
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          float ga[4], gb[4];
-          ga_[u].get(ga);
-          gb_[u].get(gb);
-          if (LAYOUT != LAYOUT_NONE && part < 2 && m.rotated) rotate<LAYOUT>(ga, gb, c, s);
+          uint64_t g[4], dy[4];
+          ga[u].pairs(g[0], g[1]);
+          gb[u].pairs(g[2], g[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dy[k] = turned ? f2_fma(P[k], g[k], f2_mul(Q[k], partner<LAYOUT>(g, k))) : g[k];
           if (nm) {
-            float xa[4], xb[4], ss = 0.0f, sd = 0.0f;
-            xa_[u].get(xa);
-            xb_[u].get(xb);
+            uint64_t x[4], t[4];
+            xa[u].pairs(x[0], x[1]);
+            xb[u].pairs(x[2], x[3]);
+            uint64_t ss = 0, sd = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              ss += xa[i] * xa[i] + xb[i] * xb[i];
-              sd += ga[i] * wa[i] * xa[i] + gb[i] * wb[i] * xb[i];
+            for (int k = 0; k < 4; ++k) {
+              t[k] = f2_mul(dy[k], x[k]);
+              ss = f2_fma(x[k], x[k], ss);
+              sd = f2_fma(t[k], W[k], sd);
             }
-            ss = row_sum<GS>(ss);
-            sd = row_sum<GS>(sd);
-            const float r = rsqrtf(ss * p.inv_d + p.eps);
-            const float k = r * r * sd * p.inv_d;
+            float s0, s1, d0, d1;
+            f2_unpack(ss, s0, s1);
+            f2_unpack(sd, d0, d1);
+            const float r = rsqrtf(row_sum<GS>(s0 + s1) * p.inv_d + p.eps);
+            const float k3 = -r * r * r * row_sum<GS>(d0 + d1) * p.inv_d;
+            const uint64_t rr = f2_pack(r, r), kk = f2_pack(k3, k3);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dwa[i] += ga[i] * xa[i] * r;
-              dwb[i] += gb[i] * xb[i] * r;
-              ga[i] = r * (ga[i] * wa[i] - xa[i] * k);
-              gb[i] = r * (gb[i] * wb[i] - xb[i] * k);
+            for (int k = 0; k < 4; ++k) {
+              dW[k] = f2_fma(t[k], rr, dW[k]);
+              dy[k] = f2_fma(x[k], kk, f2_mul(f2_mul(dy[k], W[k]), rr));
             }
           }
           if (m.on && live && h0 + u < to) {
             T* dst = drow0 + (h0 + u) * p.d;
-            store4(dst + m.a, ga);
-            store4(dst + m.b, gb);
+            store_pairs(dst + m.a, dy[0], dy[1]);
+            store_pairs(dst + m.b, dy[2], dy[3]);
           }
         }
       }
       if (nm && live) {
-        float4* mine = &acc[part][0][threadIdx.x];
-        float4 t = mine[0];
-        mine[0] = make_float4(t.x + dwa[0], t.y + dwa[1], t.z + dwa[2], t.w + dwa[3]);
-        t = mine[kThreads];
-        mine[kThreads] = make_float4(t.x + dwb[0], t.y + dwb[1], t.z + dwb[2], t.w + dwb[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float4* mine = &acc[part][i][threadIdx.x];
+          const float4 t = *mine;
+          float a, b2, c2, d2;
+          f2_unpack(dW[2 * i], a, b2);
+          f2_unpack(dW[2 * i + 1], c2, d2);
+          *mine = make_float4(t.x + a, t.y + b2, t.z + c2, t.w + d2);
+        }
       }
     }
   }
