@@ -241,21 +241,21 @@ HssaLayout hssa_layout(const bsa_shape_t* s, int km, int topk, int num_sms) {
 }
 
 // Workspace of the decode over the quantised cache: the sequences' first list
-// positions, then two partial records per block of threads and head.
+// positions, then two partial records per range and head.
 struct QuantLayout {
   size_t pre, partial, total;
-  int num_ctas;
+  QuantSplit split;
 };
 
-QuantLayout quant_layout(const bsa_shape_t* s, int num_sms) {
+QuantLayout quant_layout(const bsa_shape_t* s, bool list, int num_sms) {
   QuantLayout L{};
-  const int forced = g_split_override.load(std::memory_order_relaxed);
-  L.num_ctas = forced > 0 ? forced : quant_decode_ctas(num_sms, s->Hq / s->Hkv);
+  L.split = quant_decode_split(num_sms, s->Hq / s->Hkv, s->B * s->Hkv, list,
+                               g_split_override.load(std::memory_order_relaxed));
   size_t off = 0;
   L.pre = off;
   off = align256(off + (static_cast<size_t>(s->B) + 1) * sizeof(int));
   L.partial = off;
-  off = align256(off + static_cast<size_t>(L.num_ctas) * 2 * (s->Hq / s->Hkv) * (s->d + 4) * sizeof(float));
+  off = align256(off + static_cast<size_t>(L.split.ranges) * 2 * (s->Hq / s->Hkv) * (s->d + 4) * sizeof(float));
   L.total = off;
   return L;
 }
@@ -360,7 +360,7 @@ size_t bsa_workspace_bytes(int op, const bsa_shape_t* s, int budget) {
     if (budget < 1) return 0;
     return heads_layout(s, budget, sms).total;
   }
-  if (op == BSA_OP_DECODE_QUANT) return quant_layout(s, sms).total;
+  if (op == BSA_OP_DECODE_QUANT) return quant_layout(s, budget > 0, sms).total;
   return 0;
 }
 
@@ -1030,7 +1030,7 @@ bsa_status_t bsa_sparse_attn_decode_quant(const bsa_shape_t* s, const void* q, c
   QuantDecodeArgs a{};
   int sms = 0;
   if ((st = device_state(&a.status, &sms)) != BSA_OK) return st;
-  const QuantLayout L = quant_layout(s, sms);
+  const QuantLayout L = quant_layout(s, idx != nullptr, sms);
   if (workspace_bytes < L.total) return BSA_ERR_INVALID_ARG;
   a.B = s->B;
   a.Hq = s->Hq;
@@ -1048,7 +1048,9 @@ bsa_status_t bsa_sparse_attn_decode_quant(const bsa_shape_t* s, const void* q, c
   a.idx = idx;
   a.list_len = idx_stride;
   a.scale_log2 = softmax_scale * 1.44269504088896340736f;
-  a.num_ctas = L.num_ctas;
+  a.num_ranges = L.split.ranges;
+  a.num_ctas = L.split.ctas;
+  a.team_warps = L.split.team_warps;
   a.pre = reinterpret_cast<int*>(static_cast<char*>(workspace) + L.pre);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.partial);
   a.o = static_cast<__nv_bfloat16*>(o);

@@ -34,10 +34,12 @@
 // unrounded; logits, O and l are fp32.
 //
 // Work split: the rows' list positions are laid end to end, each sequence
-// with the blocks it has, and cut into equal ranges, one per block of
-// threads.  A range that holds a whole row writes its output; a row cut by
-// range borders leaves one partial record (M, l, O) per range, at most two a
-// block, and the second kernel joins them.
+// with the blocks it has, and cut into equal ranges, one per team of warps: a
+// block of threads is one team, or two or four where there are many rows, so
+// that a team has about a row and another team's loads fill the time in which
+// it joins its warps.  A range that holds a whole row writes its output; a row
+// cut by range borders leaves one partial record (M, l, O) per range, at most
+// two a team, and the second kernel joins them.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -46,16 +48,15 @@
 namespace bsa {
 namespace qdecode {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr float kLift = 8.0f;        // weights are 2^(y - M + 8)
 constexpr float kHeadroom = 7.0f;    // M moves when y > M + 7: weights stay below 2^15
 
-// NB = sets of eight query heads a warp carries.  One set leaves the registers
-// for two blocks an SM; two sets (groups of 9 to 16 heads) take one block with
-// twice the stages, and each code is still converted once.
-__host__ __device__ constexpr int ctas_per_sm(int NB) { return NB == 1 ? 2 : 1; }
-__host__ __device__ constexpr int stages(int NB) { return NB == 1 ? 3 : 6; }
+// NB = sets of eight query heads a warp carries; one block an SM: 16 warps of
+// two stages (three stages: 97 kept blocks x 16 sequences 41.6 us against 40.2),
+// or, where two sets (groups of 9 to 16 heads) take twice the registers, 8 warps
+// of six.
+__host__ __device__ constexpr int warps(int NB) { return NB == 1 ? 16 : 8; }
+__host__ __device__ constexpr int stages(int NB) { return NB == 1 ? 2 : 6; }
 // a stage: 16 key rows, 16 value rows, their exponent bytes
 __host__ __device__ constexpr int stage_bytes(int D) { return 2 * 16 * D + 32; }
 
@@ -86,19 +87,24 @@ __device__ __forceinline__ void cp_async_wait_group() {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Ranges that `total` positions are cut into: none is empty.
-__device__ __forceinline__ int ranges(int64_t total, int ctas) {
-  return static_cast<int>(min(static_cast<int64_t>(ctas), total));
+__device__ __forceinline__ int ranges(int64_t total, int most) {
+  return static_cast<int>(min(static_cast<int64_t>(most), total));
+}
+__device__ __forceinline__ void team_sync(int team, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(threads) : "memory");
 }
 
-// First block of threads whose range [c total / C, (c+1) total / C) holds x.
-__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int C) {
+// The range c, [c total / C, (c+1) total / C), that holds x.
+__device__ __forceinline__ int range_of(int64_t x, int64_t total, int C) {
   return static_cast<int>(((x + 1) * C + total - 1) / total) - 1;
 }
 
 // Without a list, pre[b] = blocks of the sequences before b, b <= B: a
 // sequence has as many positions (of one KV head) as it has blocks.  With one
 // every sequence has list_len positions and nothing is read for the plan.
+template <int kWarps>
 __device__ __forceinline__ void plan_positions(const QuantDecodeArgs& p, int* pre, int* warp_sums) {
+  constexpr int kThreads = 32 * kWarps;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -143,7 +149,7 @@ __device__ __forceinline__ int v_swizzle(int row) {
   return D == 128 ? (row & 6) : ((row >> 2) & 1) * 2;
 }
 
-// One row's stretch of list positions inside a block's range.
+// One row's stretch of list positions inside a range.
 struct Item {
   int b, g, w, t0, t1;
   int64_t next;      // first position behind it
@@ -181,7 +187,8 @@ __device__ __forceinline__ int pair_at(int r, int mb, int c) {
 }
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const QuantDecodeArgs p) {
+__global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDecodeArgs p) {
+  constexpr int kWarps = warps(NB), kThreads = 32 * kWarps;
   constexpr int KH = D / 64;        // 64-byte halves of a row
   constexpr int KS = D / 16;        // k-steps of q . K
   constexpr int MB = D / 16;        // 16-channel row blocks of O
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const
   int* pre = reinterpret_cast<int*>(smem_raw + kWarps * R * SB);
   griddep_wait();   // lists, lengths and the cache come from the kernels launched before
   if (p.idx == nullptr) {
-    plan_positions(p, pre, warp_sums);
+    plan_positions<kWarps>(p, pre, warp_sums);
     if (blockIdx.x == 0)
       for (int b = threadIdx.x; b <= p.B; b += kThreads) p.pre[b] = pre[b];
   }
@@ -202,10 +209,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const
   const int r = lane >> 2, c = lane & 3;
   const int G = p.Hq / p.Hkv;
   const int64_t total = static_cast<int64_t>(p.idx ? p.B * p.list_len : pre[p.B]) * p.Hkv;
-  const int C = ranges(total, gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= C) return;
-  int64_t x = blockIdx.x * total / C;
-  const int64_t hi = (blockIdx.x + 1) * total / C;
+  // teams: the first of every block, then the second of every block, ...
+  const int team_warps = p.team_warps, team = warp / team_warps, tw = warp - team * team_warps;
+  const int range = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  const int C = ranges(total, p.num_ranges);
+  if (range >= C) return;
+  int64_t x = range * total / C;
+  const int64_t hi = (range + 1) * total / C;
   int b_first = 0;
   if (p.idx == nullptr) {   // the sequence of position x: the last b with pre[b] * Hkv <= x
     int hi_b = p.B;
@@ -215,13 +225,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const
     }
   }
 
-  // ---- the loading side, R chunks ahead of the other: an item's chunks of 16 keys go to the warps in turn, a warp
-  // looks 32 of its own up at once (one a lane), and runs on into the block's next items by itself
+  // ---- the loading side, R chunks ahead of the other: an item's chunks of 16 keys go to the team's warps in
+  // turn, a warp looks 32 of its own up at once (one a lane), and runs on into the team's next items by itself
   uint8_t* ring = smem_raw + warp * R * SB;
   const uint32_t ring_u32 = smem_u32(ring);
   Item li = item_at(p, pre, x, hi, b_first);   // item being loaded
   int l_no = 0;                                 // its number
-  int l_base = warp - 32 * kWarps;              // first chunk of the batch held
+  int l_base = tw - 32 * team_warps;            // first chunk of the batch held
   int l_len = 0;
   unsigned l_left = 0u;                         // lanes whose chunk is still to be taken
   int my_row = 0, my_n = 0;                     // the lane's chunk: row of 16 in the pools, keys that count
@@ -231,19 +241,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const
   auto refill = [&](int slot) {
     bool have = true;
     while (l_left == 0u) {
-      l_base += 32 * kWarps;
+      l_base += 32 * team_warps;
       if (l_base >= 4 * (li.t1 - li.t0)) {
         if (li.next >= hi) {
           have = false;
-          l_base -= 32 * kWarps;
+          l_base -= 32 * team_warps;
           break;
         }
         li = item_at(p, pre, li.next, hi, li.b);
         l_len = seq_len(li.b);
         ++l_no;
-        l_base = warp;
+        l_base = tw;
       }
-      const int u = l_base + lane * kWarps;
+      const int u = l_base + lane * team_warps;
       my_n = 0;
       if (u < 4 * (li.t1 - li.t0)) {
         const int t = li.t0 + (u >> 2);
@@ -489,20 +499,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const
           for (int h = 0; h < 2; ++h)
             mine[(2 * c + h) * (D / 2) + pair_at<D>(r, m, c)] = make_float2(O[nb][m][h], O[nb][m][2 + h]);
       }
-      __syncthreads();
-      const int heads = min(8, G - nb * 8);
-      for (int e = threadIdx.x; e < heads * (D / 2); e += kThreads) {
+      team_sync(team, 32 * team_warps);
+      const int heads = min(8, G - nb * 8), w0 = team * team_warps;
+      for (int e = threadIdx.x - 32 * w0; e < heads * (D / 2); e += 32 * team_warps) {
         const int h = e / (D / 2), pr = e - h * (D / 2);         // query head of the set, channel pair
         const int at = h * (D / 2) + pair_at<D>(pr / (D / 16), pr % (D / 16), h >> 1);
         float mx = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, sm_m[k][nb * 8 + h]);
+        for (int k = w0; k < w0 + team_warps; ++k) mx = fmaxf(mx, sm_m[k][nb * 8 + h]);
         float L = 0.0f, o0 = 0.0f, o1 = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
+#pragma unroll 4
+        for (int k = w0; k < w0 + team_warps; ++k) {
           const float mk = sm_m[k][nb * 8 + h];
           if (mk == -INFINITY) continue;      // a warp without a key: it may have no spare stage
-          const float f = exp2f(mk - mx);
+          const float f = fast_exp2(mk - mx);
           const float2 v = reinterpret_cast<const float2*>(smem_raw + (k * R + sm_slot[k]) * SB)[at];
           L += f * sm_l[k][nb * 8 + h];
           o0 += f * v.x;
@@ -515,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const
           if (p.lse && pr == 0)
             p.lse[orow] = (mx == -INFINITY) ? -INFINITY : (mx - kLift + log2f(L)) * 0.69314718055994530942f;
         } else {
-          float* rec = p.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * G + nb * 8 + h) * (D + 4);
+          float* rec = p.partial + ((static_cast<int64_t>(range) * 2 + slot) * G + nb * 8 + h) * (D + 4);
           *reinterpret_cast<float2*>(rec + 4 + 2 * pr) = make_float2(o0, o1);
           if (pr == 0) {
             rec[0] = mx;
@@ -523,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB)) decode_kernel(const
           }
         }
       }
-      __syncthreads();
+      team_sync(team, 32 * team_warps);
     }
     if (spare >= 0) refill(spare);
   }
@@ -551,9 +560,9 @@ __global__ void __launch_bounds__(D * PARTS) combine_kernel(const QuantDecodeArg
     if (p.lse && threadIdx.x == 0) p.lse[orow] = -INFINITY;
     return;
   }
-  const int C = ranges(total, p.num_ctas);
+  const int C = ranges(total, p.num_ranges);
   const int64_t x0 = static_cast<int64_t>(before) * p.Hkv + static_cast<int64_t>(g) * w;
-  const int first = cta_of(x0, total, C), n = cta_of(x0 + w - 1, total, C) - first + 1;
+  const int first = range_of(x0, total, C), n = range_of(x0 + w - 1, total, C) - first + 1;
   if (n == 1) return;
   // the row begins inside range `first` (its record 1) and goes on in the next ones (their records 0)
   const float* rec = p.partial + (static_cast<int64_t>(first) * 2 * G + h) * (D + 4);
@@ -610,20 +619,52 @@ __global__ void __launch_bounds__(D * PARTS) combine_kernel(const QuantDecodeArg
 
 template <int D, int NB>
 cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(kWarps) * stages(NB) * stage_bytes(D) +
+  const size_t smem = static_cast<size_t>(warps(NB)) * stages(NB) * stage_bytes(D) +
                       (a.idx ? 0 : (static_cast<size_t>(a.B) + 1) * sizeof(int));
   cudaError_t e = ensure_dynamic_smem<decode_kernel<D, NB>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(decode_kernel<D, NB>, dim3(a.num_ctas), dim3(kThreads), smem, st, a);
+  e = launch_dependent(decode_kernel<D, NB>, dim3(a.num_ctas), dim3(32 * warps(NB)), smem, st, a);
   if (e != cudaSuccess) return e;
   // records a row: the ranges over the rows, on average; over one round of eight they are shared out
-  if (a.num_ctas > 8 * a.B * a.Hkv) return launch_dependent(combine_kernel<D, 4>, dim3(a.B * a.Hq), dim3(4 * D), 0, st, a);
+  if (a.num_ranges > 8 * a.B * a.Hkv) return launch_dependent(combine_kernel<D, 4>, dim3(a.B * a.Hq), dim3(4 * D), 0, st, a);
   return launch_dependent(combine_kernel<D, 1>, dim3(a.B * a.Hq), dim3(D), 0, st, a);
 }
 
 }  // namespace qdecode
 
-int quant_decode_ctas(int num_sms, int group) { return qdecode::ctas_per_sm(group > 8 ? 2 : 1) * num_sms; }
+// Groups of up to 8 heads are bound by memory, and 7/8 of the multiprocessors
+// draw more from it than all (the whole cache of 16 sequences, us: 148 blocks
+// 397, 132 389, 128 371, 120 372, 96 431; bytes in flight do not change it);
+// larger groups are bound by their products and take all (424 us, 487 with
+// 128).  Teams are halved, twice at most, until there are as many as rows.
+// Ranges that end where rows end leave fewer records to join (97 kept blocks,
+// us: 128 rows on 128 ranges 40.2, on 148 42.7; 24 rows on 144 16.0, on 148
+// 19.0): from a list, where rows are equally long, as many ranges a row as fit
+// the teams, or whole rows a range, if that keeps at least 4/5 of the teams busy;
+// without one only where a row has four ranges or more (its own length may be
+// the only one).
+QuantSplit quant_decode_split(int num_sms, int group, int rows, bool list, int forced) {
+  const int NB = group > 8 ? 2 : 1;
+  const int most = NB == 2 || num_sms < 2 ? num_sms : num_sms * 7 / 8;
+  QuantSplit s;
+  s.team_warps = qdecode::warps(NB);
+  int teams = most;
+  if (forced > 0) {
+    s.ranges = forced;
+    s.ctas = forced;
+    return s;
+  }
+  for (int half = 0; half < 2 && rows > teams; ++half) {
+    s.team_warps /= 2;
+    teams *= 2;
+  }
+  s.ranges = teams;
+  const int each = (rows + teams - 1) / teams;          // rows a range, where there are more rows than teams
+  const int even = rows <= teams ? rows * (teams / rows) : (rows + each - 1) / each;
+  if (5 * even >= 4 * teams && (list || rows <= teams / 4)) s.ranges = even;
+  s.ctas = s.ranges < most ? s.ranges : most;
+  return s;
+}
 
 cudaError_t launch_attn_decode_quant(const QuantDecodeArgs& a, int d, cudaStream_t st) {
   if (a.Hq / a.Hkv > 8) return d == 64 ? qdecode::launch<64, 2>(a, st) : qdecode::launch<128, 2>(a, st);

@@ -184,14 +184,19 @@ struct QuantDecodeArgs {
   const int* idx;              // [B*Hkv][list_len] or null (every block)
   int list_len;
   float scale_log2;
-  int num_ctas;
+  int num_ranges, num_ctas, team_warps;
   int* pre;                    // workspace: [B+1]
-  float* partial;              // workspace: [num_ctas][2][G][d+4]
+  float* partial;              // workspace: [num_ranges][2][G][d+4]
   __nv_bfloat16* o;
   float* lse;
   uint32_t* status;
 };
-int quant_decode_ctas(int num_sms, int group);
+// how a call is split: ranges of list positions, the teams of warps that take one each, blocks of threads; rows =
+// B * Hkv, list: every row has the same number of positions, forced > 0: that many ranges, a block each
+struct QuantSplit {
+  int ranges, team_warps, ctas;
+};
+QuantSplit quant_decode_split(int num_sms, int group, int rows, bool list, int forced);
 cudaError_t launch_attn_decode_quant(const QuantDecodeArgs& a, int d, cudaStream_t st);
 
 // topk_lens.cu
