@@ -14,9 +14,13 @@
 // as a rule) are listed and ranked by their full keys, or, where more than 32
 // do, their lower key bits are bisected by 32 more counts over the row.
 // Equal scores: the lower index first.  NaN compares with nothing, so it ranks
-// last by itself.  2048 rows of 1300 candidates: 14.3 us; a block of 256
-// threads a row with four 8-bit histograms took 21.2, one 12-bit histogram
-// and a ranked list 22.3.
+// last by itself.  The counts run over registers; then each lane takes 64
+// consecutive columns (16 in short rows) from shared memory, keeps what is
+// above T and what rounds to it as bits, and writes its kept columns behind
+// those of the lanes before it: no step waits for another column's.  2048 rows
+// of 1300 candidates: 11.7 us; a block of 256 threads a row with four 8-bit
+// histograms took 21.2, one 12-bit histogram and a ranked list 22.3, ballots
+// column by column instead of the lanes' bits 13.9.
 #include "kernels.h"
 #include "topk.cuh"
 
@@ -71,7 +75,6 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
                                                  int* __restrict__ count_out, uint32_t* __restrict__ status) {
   griddep_wait();   // the scores come from the kernel launched before
   const int lane = threadIdx.x;
-  const unsigned below = (1u << lane) - 1u;
   const int64_t r = blockIdx.x;
   const int len = lens[r / rows_per_len];
   const int n_all = len > 0 ? (len - 1) / block + 1 : 0;
@@ -80,13 +83,15 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
   const int ncand = max(n - 1, 0);
   const float* srow = scores + r * ncols;
   const float nan = __uint_as_float(0x7FFFFFFFu);
-  // the counts run over registers; the two passes that go column by column read the scores from shared memory in
-  // short loops (unrolled over registers they outgrow the instruction cache: 25.9 us for the 2048 rows)
-  __shared__ float2 xs[PAIRS][32];
+  constexpr int kChunk = PAIRS < 32 ? PAIRS : 32;          // pairs of a lane's columns, per round
+  constexpr int kRounds = PAIRS / kChunk;
+  __shared__ float2 xs[PAIRS * 32 + PAIRS * 32 / kChunk];   // a gap behind each chunk keeps the lanes' banks apart
+  __shared__ uint32_t member_key[32];
+  auto slot = [](int pair) { return pair + pair / kChunk; };
   uint32_t x[PAIRS];
-  // 16 pairs at a time, asked for together: no branch stands between the loads
+  // 32 pairs at a time, asked for together: no branch stands between the loads
   const bool even = ncols % 2 == 0 && (reinterpret_cast<uintptr_t>(scores) & 7u) == 0;
-  constexpr int kBatch = PAIRS < 16 ? PAIRS : 16;
+  constexpr int kBatch = PAIRS < 32 ? PAIRS : 32;
 #pragma unroll
   for (int p0 = 0; p0 < PAIRS; p0 += kBatch) {
     float2 v[kBatch];
@@ -108,15 +113,15 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
     for (int p = 0; p < kBatch; ++p) {
       if (64 * (p0 + p) + 2 * lane + 1 >= ncand) v[p].y = nan;     // the row's next column, where it was read
       x[p0 + p] = pack_bf16x2(v[p].x, v[p].y);
-      xs[p0 + p][lane] = v[p];
+      xs[slot(32 * (p0 + p) + lane)] = v[p];
     }
   }
-  const int take = min(kb, ncand), pairs = (ncand + 63) / 64;
+  const int take = min(kb, ncand);
   // kept: scores that round above T; of those that round to T, full keys above `thresh`; of the keys equal to it the
   // first `ties`.  Code kNone stands below every number's: there the scores that "round to T" are the NaNs.
   constexpr uint32_t kNone = 0x007Eu;
   uint32_t t_code = 0xFFFFu, thresh = 0u;     // nothing is kept
-  int ties = 0;
+  int ties = 0, remaining = 0, members = 0;
   if (take > 0) {
     uint32_t lo = kNone, hi = max(code_max(x), kNone);
     int at_least = ncand, above = 0;           // scores >= lo, > hi
@@ -139,97 +144,128 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
       }
     }
     t_code = lo;
-    const int remaining = take - above, members = at_least - above;
-    if (lo == kNone) {
-      ties = remaining;                                   // every number, and NaNs (key 0) in index order
-    } else if (at_least != take) {
-      if (members <= 32) {
-        // lane i takes the i-th member's full key
-        const __nv_bfloat162 t2 = as_pair(code_value(t_code) * 0x10001u);
-        int at = 0, seen = 0;
-#pragma unroll 4
-        for (int p = 0; p < pairs; ++p) {
-          const uint32_t eq = __heq2_mask(as_pair(pack_bf16x2(xs[p][lane].x, xs[p][lane].y)), t2);
-          if (__ballot_sync(0xffffffffu, eq != 0u) == 0u) continue;
-          for (int h = 0; h < 2; ++h) {
-            unsigned who = __ballot_sync(0xffffffffu, (h ? eq >> 16 : eq & 0xFFFFu) != 0u);
-            while (who) {
-              const int src = __ffs(who) - 1;
-              who &= who - 1;
-              at = lane == seen ? 64 * p + 2 * src + h : at;
-              ++seen;
-            }
-          }
+    remaining = take - above;
+    members = at_least - above;
+    if (lo == kNone) ties = remaining;        // every number, and NaNs (key 0) in index order
+  }
+  // this lane's columns, round by round: bits of those that round above T, and to T
+  __syncwarp();
+  const __nv_bfloat162 t2 = as_pair(code_value(t_code) * 0x10001u);
+  uint64_t gt[kRounds], eq[kRounds];
+#pragma unroll
+  for (int rd = 0; rd < kRounds; ++rd) {
+    gt[rd] = eq[rd] = 0u;
+    const int pair0 = (rd * 32 + lane) * kChunk;       // of this lane
+    const int left = ncand - 2 * pair0;                // its candidates
+    if (left > 0 && take > 0) {
+#pragma unroll 8
+      for (int i = 0; i < kChunk; ++i) {
+        const float2 f = xs[slot(pair0 + i)];
+        const __nv_bfloat162 v = as_pair(pack_bf16x2(f.x, f.y));
+        uint32_t above_t, at_t;
+        if (t_code == kNone) {
+          above_t = __heq2_mask(v, v);
+          at_t = ~above_t;
+        } else {
+          above_t = __hgt2_mask(v, t2);
+          at_t = __heq2_mask(v, t2);
         }
-        __syncwarp();
-        const uint32_t mine = order_key(reinterpret_cast<const float*>(xs)[at]);
-        int more = 0, same = 0;
-        for (int i = 0; i < members; ++i) {
-          const uint32_t other = __shfl_sync(0xffffffffu, mine, i);
-          more += other > mine ? 1 : 0;
-          same += other == mine ? 1 : 0;
-        }
-        const bool is_it = lane < members && more < remaining && remaining <= more + same;
-        const int src = __ffs(__ballot_sync(0xffffffffu, is_it)) - 1;
-        thresh = __shfl_sync(0xffffffffu, mine, src);
-        ties = remaining - __shfl_sync(0xffffffffu, more, src);
-      } else {
-        // many scores round to T: bisect the full keys
-        int count = 0;
-        for (int bit = 31; bit >= 0; --bit) {
-          const uint32_t cand = thresh | (1u << bit);
-          int c = 0;
-          for (int p = 0; p < pairs; ++p) {
-            c += (order_key(xs[p][lane].x) >= cand ? 1 : 0) + (order_key(xs[p][lane].y) >= cand ? 1 : 0);
-          }
-          c = __reduce_add_sync(0xffffffffu, c);
-          if (c >= take) thresh = cand;
-        }
-        for (int p = 0; p < pairs; ++p)      // what is no candidate is NaN here, key 0
-          count += (order_key(xs[p][lane].x) > thresh ? 1 : 0) + (order_key(xs[p][lane].y) > thresh ? 1 : 0);
-        ties = take - __reduce_add_sync(0xffffffffu, count);
+        // a half of the mask is all ones or zeros: bits 0 and 31 tell
+        gt[rd] |= static_cast<uint64_t>((above_t & 1u) | (above_t >> 31 << 1)) << (2 * i);
+        eq[rd] |= static_cast<uint64_t>((at_t & 1u) | (at_t >> 31 << 1)) << (2 * i);
       }
-    }                                   // else all that round to T are kept: no number's key is 0
+      if (left < 64) {
+        const uint64_t own = (1ull << left) - 1ull;
+        gt[rd] &= own;
+        eq[rd] &= own;
+      }
+    }
+  }
+  auto key_at = [&](int rd, int bit) {
+    const float2 f = xs[slot((rd * 32 + lane) * kChunk + (bit >> 1))];
+    return order_key(bit & 1 ? f.y : f.x);
+  };
+  if (t_code != kNone && remaining < members) {
+    if (members <= 32) {
+      // the members' full keys in a list, each ranked against all
+      int mine_n = 0;
+#pragma unroll
+      for (int rd = 0; rd < kRounds; ++rd) mine_n += __popcll(eq[rd]);
+      int at = mine_n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+      }
+      at -= mine_n;
+#pragma unroll
+      for (int rd = 0; rd < kRounds; ++rd)
+        for (uint64_t m = eq[rd]; m; m &= m - 1) member_key[at++] = key_at(rd, __ffsll(m) - 1);
+      __syncwarp();
+      const uint32_t mine = lane < members ? member_key[lane] : 0u;
+      int more = 0, same = 0;
+      for (int i = 0; i < members; ++i) {
+        const uint32_t other = member_key[i];
+        more += other > mine ? 1 : 0;
+        same += other == mine ? 1 : 0;
+      }
+      const bool is_it = lane < members && more < remaining && remaining <= more + same;
+      const int src = __ffs(__ballot_sync(0xffffffffu, is_it)) - 1;
+      thresh = __shfl_sync(0xffffffffu, mine, src);
+      ties = remaining - __shfl_sync(0xffffffffu, more, src);
+    } else {
+      // many scores round to T: bisect their full keys
+      int over = 0;
+      for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t cand = thresh | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int rd = 0; rd < kRounds; ++rd)
+          for (uint64_t m = eq[rd]; m; m &= m - 1) c += key_at(rd, __ffsll(m) - 1) >= cand ? 1 : 0;
+        if (__reduce_add_sync(0xffffffffu, c) >= remaining) thresh = cand;
+      }
+#pragma unroll
+      for (int rd = 0; rd < kRounds; ++rd)
+        for (uint64_t m = eq[rd]; m; m &= m - 1) over += key_at(rd, __ffsll(m) - 1) > thresh ? 1 : 0;
+      ties = remaining - __reduce_add_sync(0xffffffffu, over);
+    }
   }
   int* out = idx_out + r * idx_stride;
   int kept = 0, equal = 0;
-  const __nv_bfloat162 t2 = as_pair(code_value(t_code) * 0x10001u);
-#pragma unroll 2
-  for (int p = 0; p < pairs; ++p) {
-    const int j = 64 * p + 2 * lane;
-    const float2 f = xs[p][lane];
-    const __nv_bfloat162 v = as_pair(pack_bf16x2(f.x, f.y));
-    const uint32_t num = __heq2_mask(v, v);
-    uint32_t gt, eq;       // halves: rounds above T, rounds to T
-    if (t_code == kNone) {
-      gt = num;
-      eq = ~num;
-    } else {
-      gt = __hgt2_mask(v, t2);
-      eq = __heq2_mask(v, t2);
+#pragma unroll
+  for (int rd = 0; rd < kRounds; ++rd) {
+    uint64_t sel = gt[rd], tie = 0u;
+    if (__any_sync(0xffffffffu, eq[rd] != 0u)) {
+      for (uint64_t m = eq[rd]; m; m &= m - 1) {
+        const uint32_t key = key_at(rd, __ffsll(m) - 1);
+        const uint64_t bit = m & (0ull - m);
+        if (key > thresh) sel |= bit;
+        if (key == thresh) tie |= bit;
+      }
+      // ties in index order: the first of those not yet taken by columns before this lane's
+      const int nt = __popcll(tie);
+      int before = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      const int all = __shfl_sync(0xffffffffu, before, 31);
+      before += equal - nt;
+      for (; tie != 0u && before < ties; tie &= tie - 1, ++before) sel |= tie & (0ull - tie);
+      equal += all;
     }
-    bool sel[2] = {(gt & 0xFFFFu) != 0u, (gt >> 16) != 0u};
-    const bool mem[2] = {(eq & 0xFFFFu) != 0u && j < ncand, (eq >> 16) != 0u && j + 1 < ncand};
-    if (__ballot_sync(0xffffffffu, mem[0] || mem[1]) != 0u) {
-      bool tie[2] = {false, false};
-      for (int h = 0; h < 2; ++h)
-        if (mem[h]) {
-          const uint32_t key = order_key(h ? f.y : f.x);
-          sel[h] = key > thresh;
-          tie[h] = key == thresh;
-        }
-      // ties in index order: lane l's two columns lie between its neighbours'
-      const unsigned b0 = __ballot_sync(0xffffffffu, tie[0]), b1 = __ballot_sync(0xffffffffu, tie[1]);
-      const int before = equal + __popc(b0 & below) + __popc(b1 & below);
-      sel[0] |= tie[0] && before < ties;
-      sel[1] |= tie[1] && before + (tie[0] ? 1 : 0) < ties;
-      equal += __popc(b0) + __popc(b1);
+    const int ns = __popcll(sel);
+    int at = ns;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += v;
     }
-    const unsigned s0 = __ballot_sync(0xffffffffu, sel[0]), s1 = __ballot_sync(0xffffffffu, sel[1]);
-    const int at = kept + __popc(s0 & below) + __popc(s1 & below);
-    if (sel[0]) out[at] = j;
-    if (sel[1]) out[at + (sel[0] ? 1 : 0)] = j + 1;
-    kept += __popc(s0) + __popc(s1);
+    const int all = __shfl_sync(0xffffffffu, at, 31);
+    at += kept - ns;
+    for (; sel; sel &= sel - 1) out[at++] = (rd * 32 + lane) * 2 * kChunk + __ffsll(sel) - 1;
+    kept += all;
   }
   if (n > 0) {
     if (lane == 0) out[kept] = n - 1;
