@@ -42,6 +42,10 @@ __host__ __device__ constexpr int fwd_ctas() {
   return sizeof(T) == 2 ? 4 : 3;
 }
 constexpr int kBwdCtasPerSm = 2;
+template <typename T>
+__host__ __device__ constexpr int bwd_rows() {
+  return sizeof(T) == 2 ? 4 : 2;
+}
 
 enum { LAYOUT_NONE = 0, LAYOUT_HALF = 1, LAYOUT_PAIRS = 2 };
 
@@ -179,8 +183,10 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Work items: token tiles (kThreads/GS tokens, one per lane group) x runs of
-// head_run heads.
+// Forward: one block per token tile (kThreads / GS tokens, one per lane group)
+// and run of head_run heads.  Blocks that start as others end do better here
+// than resident ones with even shares (144 us against 181 for 32K tokens: these
+// run in step, all loading or all storing, and the split costs registers).
 template <typename T, int GS, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, fwd_ctas<T>()) fwd_kernel(const NormRopeArgs p) {
   griddep_wait();
@@ -277,7 +283,38 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas<T>()) fwd_kernel(const Norm
   }
 }
 
-// Backward.  Persistent over (token tile, head run) items.  The weights'
+// Work split of the backward: token tiles x heads, laid end to end tile by tile
+// in units of head_run heads and cut into one even range a block, all blocks
+// resident at once; a block forms a token's angles once for each stretch of its
+// heads.
+struct Stretch {
+  int64_t tile;
+  int h_begin, h_end;
+};
+struct Range {
+  int64_t x, hi;
+  int units, run, H;
+  __device__ __forceinline__ Range(const NormRopeArgs& p, int tile_tokens) {
+    H = p.Hq + 2 * p.Hkv;
+    run = p.head_run;
+    units = (H + run - 1) / run;
+    const int64_t tiles = (static_cast<int64_t>(p.B) * p.N + tile_tokens - 1) / tile_tokens;
+    x = blockIdx.x * (tiles * units) / gridDim.x;
+    hi = (blockIdx.x + 1) * (tiles * units) / gridDim.x;
+  }
+  __device__ __forceinline__ bool next(Stretch& t) {
+    if (x >= hi) return false;
+    t.tile = x / units;
+    const int u0 = static_cast<int>(x - t.tile * units);
+    const int u1 = static_cast<int>(min(static_cast<int64_t>(units), u0 + (hi - x)));
+    t.h_begin = u0 * run;
+    t.h_end = min(u1 * run, H);
+    x += u1 - u0;
+    return true;
+  }
+};
+
+// Backward.  The weights'
 // gradients of a lane's channels are summed in registers over the heads of a
 // token and added to the lane's own place in shared memory token by token
 // (which frees half of the registers that sums over all rows would hold); the
@@ -287,28 +324,23 @@ template <typename T, int GS, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const NormRopeArgs p) {
   griddep_wait();
   constexpr int kTokens = kThreads / GS;
-  constexpr int kRows = sizeof(T) == 2 ? 4 : 2;   // rows a lane has in flight (their fp32 gradients and inputs)
+  constexpr int kRows = bwd_rows<T>();   // rows a lane has in flight (their fp32 gradients and inputs)
   __shared__ float4 acc[2][2][kThreads];   // [weight][piece][thread]
   __shared__ unsigned long long freqs[kMaxPairs];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS;
   const Lane m = lane_channels<LAYOUT>(l, p.d, p.rot);
-  const int64_t tokens = static_cast<int64_t>(p.B) * p.N;
-  const int64_t tiles = (tokens + kTokens - 1) / kTokens;
-  const int H = p.Hq + 2 * p.Hkv;
-  const int runs = (H + p.head_run - 1) / p.head_run;
   const bool norm = p.q_weight != nullptr;
   if (LAYOUT != LAYOUT_NONE) block_freqs(p.inv_freq, p.rot / 2, freqs);
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int64_t item = blockIdx.x; item < tiles * runs; item += gridDim.x) {
-    const int64_t tile = item / runs;
-    const int run = static_cast<int>(item - tile * runs);
-    const int64_t token = tile * kTokens + grp;
-    const bool live = token < tokens;
+  Range work(p, kTokens);
+  for (Stretch st; work.next(st);) {
+    const int64_t token = st.tile * kTokens + grp;
+    const bool live = token < static_cast<int64_t>(p.B) * p.N;
     const int64_t tk = live ? token : 0;
     const int b = static_cast<int>(tk / p.N);
     const int n = static_cast<int>(tk - static_cast<int64_t>(b) * p.N);
-    const int h_begin = run * p.head_run, h_end = min(h_begin + p.head_run, H);
+    const int h_begin = st.h_begin, h_end = st.h_end;
     const T* row0 = static_cast<const T*>(p.qkv) + tk * p.token_stride;
     T* drow0 = static_cast<T*>(p.d_qkv) + tk * p.d_token_stride;
     uint64_t P[4] = {}, Q[4] = {};
@@ -451,17 +483,22 @@ cudaError_t launch(NormRopeArgs p, bool bwd, int num_sms, cudaStream_t st) {
   constexpr int kTokens = kThreads / GS;
   const int64_t tiles = (static_cast<int64_t>(p.B) * p.N + kTokens - 1) / kTokens;
   const int H = p.Hq + 2 * p.Hkv;
-  // heads of one token are split over blocks only while the token tiles alone
-  // leave multiprocessors without two blocks
-  int runs = 1;
-  while (runs < H && tiles * runs < 2 * num_sms) runs *= 2;
-  p.head_run = (H + runs - 1) / runs;
-  runs = (H + p.head_run - 1) / p.head_run;
-  if (!bwd)
-    return launch_dependent(fwd_kernel<T, GS, LAYOUT>, dim3(static_cast<unsigned>(tiles), runs), dim3(kThreads), 0, st,
-                            p);
-  const int64_t items = tiles * runs;
-  const int grid = static_cast<int>(items < norm_rope_bwd_blocks(num_sms) ? items : norm_rope_bwd_blocks(num_sms));
+  if (!bwd) {
+    // heads of one token are split over blocks only while the token tiles alone leave multiprocessors without two
+    // blocks: each split forms the angles again
+    int runs = 1;
+    while (runs < H && tiles * runs < 2 * num_sms) runs *= 2;
+    p.head_run = (H + runs - 1) / runs;
+    return launch_dependent(fwd_kernel<T, GS, LAYOUT>,
+                            dim3(static_cast<unsigned>(tiles), (H + p.head_run - 1) / p.head_run), dim3(kThreads), 0,
+                            st, p);
+  }
+  // units of as many heads as a lane has in flight, fewer where that leaves blocks without work (single tokens)
+  const int slots = norm_rope_bwd_blocks(num_sms);
+  p.head_run = bwd_rows<T>();
+  while (p.head_run > 1 && tiles * ((H + p.head_run - 1) / p.head_run) < slots) --p.head_run;
+  const int64_t items = tiles * ((H + p.head_run - 1) / p.head_run);
+  const int grid = static_cast<int>(items < slots ? items : slots);
   cudaError_t e = launch_dependent(bwd_kernel<T, GS, LAYOUT>, dim3(grid), dim3(kThreads), 0, st, p);
   if (e != cudaSuccess || p.q_weight == nullptr) return e;
   return launch_dependent(dw_reduce_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, st, p.dw_partial, grid, p.d,
