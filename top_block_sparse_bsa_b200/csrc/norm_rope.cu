@@ -12,13 +12,14 @@
 //
 // Both passes are bound by memory: every value is read once and written once
 // and a row needs about 10 operations a channel.  So a row lives in the
-// registers of d/8 lanes (rounded up to 8, 16 or 32), eight channels a lane in
-// two pieces of four.  In the half layout a lane's pieces are channels i..i+3
-// and their partners rot_dim/2 further, so the rotation needs no exchange
-// between lanes; the sums of the norm are shuffles inside the row's lanes.
-// A lane keeps its channels from head to head, so the cosines and sines of a
-// token are computed once per lane and serve all its heads: no table of
-// angles is read.
+// registers of a few lanes, 2 E channels a lane in two pieces of E = 4 or 8.  In
+// the half layout a lane's pieces are channels i..i+E-1 and their partners
+// rot_dim/2 further, so the rotation needs no exchange between lanes; the sums
+// of the norm are shuffles inside the row's lanes.  A lane keeps its channels
+// from head to head, so the cosines and sines of a token are computed once per
+// lane and serve all its heads: no table of angles is read.  32K tokens of 48
+// heads, bf16: 135 us, 91% of the copy rate; fp32 252 us, 97%; the backward of
+// 32K tokens of 36 heads 202 us, 88%.
 //
 // Angles.  position * inv_freq reaches 1e6 radians and more, where an fp32
 // product is off by 0.06.  The frequency in turns, modulo one, is held as a
@@ -31,15 +32,17 @@ namespace bsa {
 namespace nrope {
 
 constexpr int kThreads = 256;
-// rows a lane of the forward has in flight, and blocks an SM (32K tokens of 48 heads, us): bf16 4 rows x 4 blocks 144,
-// 4 x 3 142, 3 x 4 147, 2 x 5 145, 8 x 2 149, 6 x 3 155; fp32 3 x 3 252, 4 x 3 257, 4 x 4 280
-template <typename T>
+// Rows a lane of the forward has in flight, and blocks an SM (32K tokens of 48
+// heads, us): bf16 in 16-byte pieces 4 rows x 2 blocks 135, 3 x 2 147, 5 x 2 143,
+// 6 x 2 150, 2 x 3 154; in 8-byte pieces 4 x 4 143, 3 x 4 147, 2 x 5 145; fp32
+// 3 x 3 252, 4 x 3 257, 4 x 4 280.
+template <typename T, int E>
 __host__ __device__ constexpr int fwd_rows() {
-  return sizeof(T) == 2 ? 4 : 3;
+  return sizeof(T) == 4 ? 3 : 4;
 }
-template <typename T>
+template <typename T, int E>
 __host__ __device__ constexpr int fwd_ctas() {
-  return sizeof(T) == 2 ? 4 : 3;
+  return sizeof(T) == 4 ? 3 : (E == 8 ? 2 : 4);
 }
 constexpr int kBwdCtasPerSm = 2;
 template <typename T>
@@ -49,81 +52,92 @@ __host__ __device__ constexpr int bwd_rows() {
 
 enum { LAYOUT_NONE = 0, LAYOUT_HALF = 1, LAYOUT_PAIRS = 2 };
 
-// Four consecutive channels of a row, kept as loaded: a bf16 piece waits for
-// its turn in two registers.  pairs() gives them as two packed fp32 pairs.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<float> {
-  float4 v;
-  __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
-  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
-  __device__ __forceinline__ void pairs(uint64_t& lo, uint64_t& hi) const {
-    lo = f2_pack(v.x, v.y);
-    hi = f2_pack(v.z, v.w);
+// E consecutive channels of a row, kept as loaded: a bf16 piece waits for its
+// turn in half of the registers.  pairs() gives them as packed fp32 pairs.
+template <typename T, int E>
+struct Raw {
+  static constexpr int kWords = E * static_cast<int>(sizeof(T)) / 4;
+  static_assert(kWords == 2 || kWords == 4, "a piece is one 8- or 16-byte access");
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
-};
-template <>
-struct Raw<__nv_bfloat16> {
-  uint2 v;
-  __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = v; }
-  __device__ __forceinline__ void pairs(uint64_t& lo, uint64_t& hi) const {
-    lo = f2_pack(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
-    hi = f2_pack(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kWords == 2)
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void pairs(uint64_t* x) const {
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k)
+      x[k] = sizeof(T) == 2 ? f2_pack(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u))
+                            : f2_pack(__uint_as_float(w[(2 * k) % kWords]), __uint_as_float(w[(2 * k + 1) % kWords]));
   }
 };
 // The one rounding of the operator: fp32 results to the output's type.
-__device__ __forceinline__ void store_pairs(float* p, uint64_t lo, uint64_t hi) {
-  float4 v;
-  f2_unpack(lo, v.x, v.y);
-  f2_unpack(hi, v.z, v.w);
-  *reinterpret_cast<float4*>(p) = v;
-}
-__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, uint64_t lo, uint64_t hi) {
-  float a, b, c, d;
-  f2_unpack(lo, a, b);
-  f2_unpack(hi, c, d);
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+template <typename T, int E>
+__device__ __forceinline__ void store_pairs(T* p, const uint64_t* x) {
+  Raw<T, E> r;
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) {
+    float lo, hi;
+    f2_unpack(x[k], lo, hi);
+    if constexpr (sizeof(T) == 2) {
+      r.w[k] = pack_bf16x2(lo, hi);
+    } else {
+      r.w[2 * k] = __float_as_uint(lo);
+      r.w[2 * k + 1] = __float_as_uint(hi);
+    }
+  }
+  r.store(p);
 }
 
-// The channels of one lane: pieces [a, a+4) and [b, b+4); `on`: they exist;
-// `rotated`: they belong to the rotated part.  rot is a multiple of 8.
+// The channels of one lane: pieces [a, a+E) and [b, b+E); `on`: they exist;
+// `rotated`: they belong to the rotated part.  d and rot are multiples of 2 E.
 struct Lane {
   int a, b;
   bool on, rotated;
 };
-template <int LAYOUT>
+template <int LAYOUT, int E>
 __device__ __forceinline__ Lane lane_channels(int l, int d, int rot) {
   Lane m;
-  if (LAYOUT == LAYOUT_HALF && l < rot / 8) {
-    m.a = 4 * l;
-    m.b = rot / 2 + 4 * l;
+  if (LAYOUT == LAYOUT_HALF && 2 * E * l < rot) {
+    m.a = E * l;
+    m.b = rot / 2 + E * l;
   } else {
-    m.a = 8 * l;
-    m.b = 8 * l + 4;
+    m.a = 2 * E * l;
+    m.b = 2 * E * l + E;
   }
-  m.on = 8 * l < d;
-  m.rotated = LAYOUT != LAYOUT_NONE && 8 * l < rot;
+  m.on = 2 * E * l < d;
+  m.rotated = LAYOUT != LAYOUT_NONE && 2 * E * l < rot;
   return m;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_weight(const T* __restrict__ weight, const Lane& m, float (&w)[8]) {
-  Raw<T> a, b;
+template <typename T, int E>
+__device__ __forceinline__ void load_weight(const T* __restrict__ weight, const Lane& m, float (&w)[2 * E]) {
+  Raw<T, E> a, b;
   a.load(weight + m.a);
   b.load(weight + m.b);
-  uint64_t x[4];
-  a.pairs(x[0], x[1]);
-  b.pairs(x[2], x[3]);
+  uint64_t x[E];
+  a.pairs(x);
+  b.pairs(x + E / 2);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) f2_unpack(x[k], w[2 * k], w[2 * k + 1]);
+  for (int k = 0; k < E; ++k) f2_unpack(x[k], w[2 * k], w[2 * k + 1]);
 }
 
 // Frequencies as fractions of a turn, 2^64 to the turn, in shared memory: one
-// conversion a block and pair.  A lane's four begin at 4 l.
+// conversion a block and pair.  A lane's E begin at E l.
 constexpr int kMaxPairs = 128;
 __device__ __forceinline__ void block_freqs(const double* __restrict__ inv_freq, int pairs,
                                             unsigned long long* __restrict__ f) {
@@ -134,10 +148,11 @@ __device__ __forceinline__ void block_freqs(const double* __restrict__ inv_freq,
   }
   __syncthreads();
 }
-__device__ __forceinline__ void angles(const unsigned long long* __restrict__ f, int pos, float scale, float (&c)[4],
-                                       float (&s)[4]) {
+template <int E>
+__device__ __forceinline__ void angles(const unsigned long long* __restrict__ f, int pos, float scale, float (&c)[E],
+                                       float (&s)[E]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < E; ++i) {
     const unsigned long long turns = static_cast<unsigned long long>(static_cast<long long>(pos)) * f[i];
     const int top = static_cast<int>(turns >> 32);
     float sn, cs;
@@ -146,27 +161,27 @@ __device__ __forceinline__ void angles(const unsigned long long* __restrict__ f,
     s[i] = sn * scale;
   }
 }
-// A lane's eight channels as packed pairs X[0..3] = (a0,a1) (a2,a3) (b0,b1)
-// (b2,b3).  A rotation (with factors on the channels) is P X + Q X', where X'
-// is the pair that holds X's partners: X[k ^ 2] in the half layout, X itself
-// with its two halves exchanged in the other.
-template <int LAYOUT>
-__device__ __forceinline__ uint64_t partner(const uint64_t (&x)[4], int k) {
-  if (LAYOUT == LAYOUT_HALF) return x[k ^ 2];
+// A lane's 2 E channels as packed pairs X[0..E-1], piece a's (a0,a1) (a2,a3) ...
+// and then b's.  A rotation (with factors on the channels) is P X + Q X', where
+// X' is the pair that holds X's partners: X[k ^ E/2] in the half layout, X
+// itself with its two halves exchanged in the other.
+template <int LAYOUT, int E>
+__device__ __forceinline__ uint64_t partner(const uint64_t (&x)[E], int k) {
+  if (LAYOUT == LAYOUT_HALF) return x[k ^ (E / 2)];
   float lo, hi;
   f2_unpack(x[k], lo, hi);
   return f2_pack(hi, lo);
 }
 // P and Q of the turn by (c, s) of channels whose factors are w: y = turn(w x).
-template <int LAYOUT>
-__device__ __forceinline__ void turn_factors(const float (&c)[4], const float (&s)[4], const float (&w)[8],
-                                             uint64_t (&P)[4], uint64_t (&Q)[4]) {
+template <int LAYOUT, int E>
+__device__ __forceinline__ void turn_factors(const float (&c)[E], const float (&s)[E], const float (&w)[2 * E],
+                                             uint64_t (&P)[E], uint64_t (&Q)[E]) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i0 = 2 * k, i1 = 2 * k + 1;          // the pair's channels among the lane's eight
+  for (int k = 0; k < E; ++k) {
+    const int i0 = 2 * k, i1 = 2 * k + 1;              // the pair's channels among the lane's
     if (LAYOUT == LAYOUT_HALF) {
-      const int q = i0 & 3, o = i0 ^ 4;            // angles of the pair; partners o, o + 1
-      const float sign = k < 2 ? -1.0f : 1.0f;
+      const int q = i0 & (E - 1), o = i0 ^ E;          // angles of the pair; partners o, o + 1
+      const float sign = k < E / 2 ? -1.0f : 1.0f;
       P[k] = f2_pack(w[i0] * c[q], w[i1] * c[q + 1]);
       Q[k] = f2_pack(sign * w[o] * s[q], sign * w[o + 1] * s[q + 1]);
     } else {
@@ -187,13 +202,13 @@ __device__ __forceinline__ float row_sum(float v) {
 // and run of head_run heads.  Blocks that start as others end do better here
 // than resident ones with even shares (144 us against 181 for 32K tokens: these
 // run in step, all loading or all storing, and the split costs registers).
-template <typename T, int GS, int LAYOUT>
-__global__ void __launch_bounds__(kThreads, fwd_ctas<T>()) fwd_kernel(const NormRopeArgs p) {
+template <typename T, int GS, int LAYOUT, int E>
+__global__ void __launch_bounds__(kThreads, fwd_ctas<T, E>()) fwd_kernel(const NormRopeArgs p) {
   griddep_wait();
-  constexpr int kTokens = kThreads / GS, kUnroll = fwd_rows<T>();
+  constexpr int kTokens = kThreads / GS, kUnroll = fwd_rows<T, E>();
   __shared__ unsigned long long freqs[kMaxPairs];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS;
-  const Lane m = lane_channels<LAYOUT>(l, p.d, p.rot);
+  const Lane m = lane_channels<LAYOUT, E>(l, p.d, p.rot);
   const int64_t token = static_cast<int64_t>(blockIdx.x) * kTokens + grp;
   const int64_t tokens = static_cast<int64_t>(p.B) * p.N;
   const bool live = token < tokens;      // lanes of a dead group still take part in the shuffles
@@ -202,10 +217,10 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas<T>()) fwd_kernel(const Norm
   const int n = static_cast<int>(tk - static_cast<int64_t>(b) * p.N);
   const int h_begin = blockIdx.y * p.head_run, h_end = min(h_begin + p.head_run, p.Hq + 2 * p.Hkv);
   const T* row0 = static_cast<const T*>(p.qkv) + tk * p.token_stride;
-  float c[4], s[4];
+  float c[E], s[E];
   if (LAYOUT != LAYOUT_NONE && h_begin < p.Hq + p.Hkv) {
     block_freqs(p.inv_freq, p.rot / 2, freqs);
-    if (m.rotated) angles(freqs + 4 * l, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
+    if (m.rotated) angles<E>(freqs + E * l, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
   }
   for (int part = 0; part < 3; ++part) {   // queries, keys, values
     const int lo = part == 0 ? 0 : (part == 1 ? p.Hq : p.Hq + p.Hkv);
@@ -220,21 +235,21 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas<T>()) fwd_kernel(const Norm
     const bool norm = part < 2 && weight != nullptr;
     const bool turned = LAYOUT != LAYOUT_NONE && part < 2 && m.rotated;
     // the norm's weight rides in the rotation's factors; without a rotation P is the weight alone
-    uint64_t P[4], Q[4];
+    uint64_t P[E], Q[E];
     if (part < 2) {
-      float w[8];
+      float w[2 * E];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-      if (norm && m.on) load_weight(weight, m, w);
+      for (int i = 0; i < 2 * E; ++i) w[i] = 1.0f;
+      if (norm && m.on) load_weight<T, E>(weight, m, w);
       if (turned) {
-        turn_factors<LAYOUT>(c, s, w, P, Q);
+        turn_factors<LAYOUT, E>(c, s, w, P, Q);
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) P[k] = f2_pack(w[2 * k], w[2 * k + 1]), Q[k] = 0;
+        for (int k = 0; k < E; ++k) P[k] = f2_pack(w[2 * k], w[2 * k + 1]), Q[k] = 0;
       }
     }
     for (int h0 = from; h0 < to; h0 += kUnroll, src += kUnroll * p.d, dst += kUnroll * head_step) {
-      Raw<T> ra[kUnroll], rb[kUnroll];
+      Raw<T, E> ra[kUnroll], rb[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (m.on && live && h0 + u < to) {
@@ -256,27 +271,29 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas<T>()) fwd_kernel(const Norm
           }
           continue;
         }
-        uint64_t x[4], y[4];
-        ra[u].pairs(x[0], x[1]);
-        rb[u].pairs(x[2], x[3]);
+        uint64_t x[E], y[E];
+        ra[u].pairs(x);
+        rb[u].pairs(x + E / 2);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = f2_mul(P[k], x[k]);
+        for (int k = 0; k < E; ++k) y[k] = f2_mul(P[k], x[k]);
         if (turned) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = f2_fma(Q[k], partner<LAYOUT>(x, k), y[k]);
+          for (int k = 0; k < E; ++k) y[k] = f2_fma(Q[k], partner<LAYOUT, E>(x, k), y[k]);
         }
         if (norm) {
-          const uint64_t s2 = f2_fma(x[3], x[3], f2_fma(x[2], x[2], f2_fma(x[1], x[1], f2_mul(x[0], x[0]))));
+          uint64_t s2 = f2_mul(x[0], x[0]);
+#pragma unroll
+          for (int k = 1; k < E; ++k) s2 = f2_fma(x[k], x[k], s2);
           float lo2, hi2;
           f2_unpack(s2, lo2, hi2);
           const float r = rsqrtf(row_sum<GS>(lo2 + hi2) * p.inv_d + p.eps);
           const uint64_t rr = f2_pack(r, r);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = f2_mul(y[k], rr);
+          for (int k = 0; k < E; ++k) y[k] = f2_mul(y[k], rr);
         }
         if (in) {
-          store_pairs(to_row + m.a, y[0], y[1]);
-          store_pairs(to_row + m.b, y[2], y[3]);
+          store_pairs<T, E>(to_row + m.a, y);
+          store_pairs<T, E>(to_row + m.b, y + E / 2);
         }
       }
     }
@@ -328,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
   __shared__ float4 acc[2][2][kThreads];   // [weight][piece][thread]
   __shared__ unsigned long long freqs[kMaxPairs];
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS;
-  const Lane m = lane_channels<LAYOUT>(l, p.d, p.rot);
+  const Lane m = lane_channels<LAYOUT, 4>(l, p.d, p.rot);
   const bool norm = p.q_weight != nullptr;
   if (LAYOUT != LAYOUT_NONE) block_freqs(p.inv_freq, p.rot / 2, freqs);
 #pragma unroll
@@ -346,11 +363,11 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
     uint64_t P[4] = {}, Q[4] = {};
     if (LAYOUT != LAYOUT_NONE && m.rotated && h_begin < p.Hq + p.Hkv) {
       float c[4], s[4];
-      angles(freqs + 4 * l, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
+      angles<4>(freqs + 4 * l, p.positions ? __ldg(p.positions + tk) : n, p.rope_scale, c, s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] = -s[i];       // turned back
       const float ones[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-      turn_factors<LAYOUT>(c, s, ones, P, Q);
+      turn_factors<LAYOUT, 4>(c, s, ones, P, Q);
     }
     for (int part = 0; part < 3; ++part) {
       const int lo = part == 0 ? 0 : (part == 1 ? p.Hq : p.Hq + p.Hkv);
@@ -366,13 +383,13 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
       uint64_t W[4] = {}, dW[4] = {};
       if (nm && m.on) {
         float w[8];
-        load_weight(weight, m, w);
+        load_weight<T, 4>(weight, m, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) W[k] = f2_pack(w[2 * k], w[2 * k + 1]);
       }
       for (int h0 = from; h0 < to; h0 += kRows) {
-        Raw<float> ga[kRows], gb[kRows];
-        Raw<T> xa[kRows], xb[kRows];
+        Raw<float, 4> ga[kRows], gb[kRows];
+        Raw<T, 4> xa[kRows], xb[kRows];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           ga[u].zero(), gb[u].zero(), xa[u].zero(), xb[u].zero();
@@ -389,15 +406,15 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           uint64_t g[4], dy[4];
-          ga[u].pairs(g[0], g[1]);
-          gb[u].pairs(g[2], g[3]);
+          ga[u].pairs(g);
+          gb[u].pairs(g + 2);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            dy[k] = turned ? f2_fma(P[k], g[k], f2_mul(Q[k], partner<LAYOUT>(g, k))) : g[k];
+            dy[k] = turned ? f2_fma(P[k], g[k], f2_mul(Q[k], partner<LAYOUT, 4>(g, k))) : g[k];
           if (nm) {
             uint64_t x[4], t[4];
-            xa[u].pairs(x[0], x[1]);
-            xb[u].pairs(x[2], x[3]);
+            xa[u].pairs(x);
+            xb[u].pairs(x + 2);
             uint64_t ss = 0, sd = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -419,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
           }
           if (m.on && live && h0 + u < to) {
             T* dst = drow0 + (h0 + u) * p.d;
-            store_pairs(dst + m.a, dy[0], dy[1]);
-            store_pairs(dst + m.b, dy[2], dy[3]);
+            store_pairs<T, 4>(dst + m.a, dy);
+            store_pairs<T, 4>(dst + m.b, dy + 2);
           }
         }
       }
@@ -442,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
   // thread = (weight, piece, lane of the row): its four channels over the groups in order
   for (int e = threadIdx.x; e < 4 * GS; e += kThreads) {
     const int w = e / (2 * GS), piece = e / GS % 2, le = e % GS;
-    const Lane me = lane_channels<LAYOUT>(le, p.d, p.rot);
+    const Lane me = lane_channels<LAYOUT, 4>(le, p.d, p.rot);
     if (!me.on) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -478,20 +495,31 @@ __global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* __restrict
   if (col == 0 && out < 2 * d) (out < d ? dqw[out] : dkw[out - d]) = static_cast<float>(v);
 }
 
+template <typename T, int GS, int LAYOUT, int E>
+cudaError_t launch_fwd(NormRopeArgs p, int num_sms, cudaStream_t st) {
+  constexpr int kTokens = kThreads / GS;
+  const int64_t tiles = (static_cast<int64_t>(p.B) * p.N + kTokens - 1) / kTokens;
+  const int H = p.Hq + 2 * p.Hkv;
+  // heads of one token are split over blocks only while the token tiles alone leave multiprocessors without two
+  // blocks: each split forms the angles again
+  int runs = 1;
+  while (runs < H && tiles * runs < 2 * num_sms) runs *= 2;
+  p.head_run = (H + runs - 1) / runs;
+  return launch_dependent(fwd_kernel<T, GS, LAYOUT, E>,
+                          dim3(static_cast<unsigned>(tiles), (H + p.head_run - 1) / p.head_run), dim3(kThreads), 0, st,
+                          p);
+}
+
 template <typename T, int GS, int LAYOUT>
 cudaError_t launch(NormRopeArgs p, bool bwd, int num_sms, cudaStream_t st) {
   constexpr int kTokens = kThreads / GS;
   const int64_t tiles = (static_cast<int64_t>(p.B) * p.N + kTokens - 1) / kTokens;
   const int H = p.Hq + 2 * p.Hkv;
   if (!bwd) {
-    // heads of one token are split over blocks only while the token tiles alone leave multiprocessors without two
-    // blocks: each split forms the angles again
-    int runs = 1;
-    while (runs < H && tiles * runs < 2 * num_sms) runs *= 2;
-    p.head_run = (H + runs - 1) / runs;
-    return launch_dependent(fwd_kernel<T, GS, LAYOUT>,
-                            dim3(static_cast<unsigned>(tiles), (H + p.head_run - 1) / p.head_run), dim3(kThreads), 0,
-                            st, p);
+    // 16-byte pieces of bf16 where the widths allow them
+    if constexpr (sizeof(T) == 2)
+      if (p.d % 16 == 0 && p.rot % 16 == 0) return launch_fwd<T, GS / 2, LAYOUT, 8>(p, num_sms, st);
+    return launch_fwd<T, GS, LAYOUT, 4>(p, num_sms, st);
   }
   // units of as many heads as a lane has in flight, fewer where that leaves blocks without work (single tokens)
   const int slots = norm_rope_bwd_blocks(num_sms);
