@@ -55,52 +55,63 @@ enum { LAYOUT_NONE = 0, LAYOUT_HALF = 1, LAYOUT_PAIRS = 2 };
 // E consecutive channels of a row, kept as loaded: a bf16 piece waits for its
 // turn in half of the registers.  pairs() gives them as packed fp32 pairs.
 template <typename T, int E>
-struct Raw {
-  static constexpr int kWords = E * static_cast<int>(sizeof(T)) / 4;
-  static_assert(kWords == 2 || kWords == 4, "a piece is one 8- or 16-byte access");
-  uint32_t w[kWords];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0u;
-  }
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kWords == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = v.x, w[1] = v.y;
-    } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    }
-  }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (kWords == 2)
-      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+struct Raw;
+template <>
+struct Raw<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
   __device__ __forceinline__ void pairs(uint64_t* x) const {
-#pragma unroll
-    for (int k = 0; k < E / 2; ++k)
-      x[k] = sizeof(T) == 2 ? f2_pack(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u))
-                            : f2_pack(__uint_as_float(w[(2 * k) % kWords]), __uint_as_float(w[(2 * k + 1) % kWords]));
+    x[0] = f2_pack(v.x, v.y);
+    x[1] = f2_pack(v.z, v.w);
+  }
+};
+__device__ __forceinline__ uint64_t widen(uint32_t two) {
+  return f2_pack(__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u));
+}
+template <>
+struct Raw<__nv_bfloat16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = v; }
+  __device__ __forceinline__ void pairs(uint64_t* x) const {
+    x[0] = widen(v.x);
+    x[1] = widen(v.y);
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ void pairs(uint64_t* x) const {
+    x[0] = widen(v.x);
+    x[1] = widen(v.y);
+    x[2] = widen(v.z);
+    x[3] = widen(v.w);
   }
 };
 // The one rounding of the operator: fp32 results to the output's type.
+__device__ __forceinline__ uint32_t narrow(uint64_t x) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
 template <typename T, int E>
 __device__ __forceinline__ void store_pairs(T* p, const uint64_t* x) {
-  Raw<T, E> r;
-#pragma unroll
-  for (int k = 0; k < E / 2; ++k) {
-    float lo, hi;
-    f2_unpack(x[k], lo, hi);
-    if constexpr (sizeof(T) == 2) {
-      r.w[k] = pack_bf16x2(lo, hi);
-    } else {
-      r.w[2 * k] = __float_as_uint(lo);
-      r.w[2 * k + 1] = __float_as_uint(hi);
-    }
+  if constexpr (sizeof(T) == 4) {
+    float4 v;
+    f2_unpack(x[0], v.x, v.y);
+    f2_unpack(x[1], v.z, v.w);
+    *reinterpret_cast<float4*>(p) = v;
+  } else if constexpr (E == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(narrow(x[0]), narrow(x[1]));
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(narrow(x[0]), narrow(x[1]), narrow(x[2]), narrow(x[3]));
   }
-  r.store(p);
 }
 
 // The channels of one lane: pieces [a, a+E) and [b, b+E); `on`: they exist;
