@@ -560,7 +560,7 @@ bsa_status_t bsa_paged_read_quant(const bsa_shape_t* shape, const void* k_pool, 
  *   256-byte aligned; its contents on entry do not matter; calls that may
  *   overlap need one each.
  * Built: BF16, d in {64, 128}, block = 64, at most 16 query heads per KV group,
- *   B <= 8192, num_pages * Hkv < 2^29.
+ *   B <= 8192, num_pages * Hkv < 2^29, B * idx_stride (or B * nb) < 2^29.
  */
 bsa_status_t bsa_sparse_attn_decode_quant(const bsa_shape_t* shape, const void* q, const void* k_pool,
                                           const void* v_pool, const void* k_exp, const void* v_exp, int num_pages,

@@ -443,6 +443,34 @@ def test_decode_with_other_splits(bsa, splits):
         bsa.bsa_decode_split_override(prev)
 
 
+@pytest.mark.parametrize("B,Hkv,G", [(20, 8, 4), (40, 8, 1), (80, 8, 3), (20, 8, 12), (40, 8, 16)])
+def test_decode_of_many_rows(bsa, B, Hkv, G):
+    """More rows than multiprocessors: blocks of threads split into teams, ranges with several rows each."""
+    r = np.random.default_rng(B + G)
+    lens = r.integers(0, 260, B).tolist()
+    nb, keep = 5, 3
+    q = torch.randn((B, Hkv * G, 64), generator=torch.Generator().manual_seed(G)).bfloat16()
+    cache = _cache(lens, Hkv, 64, nb, seed=B)
+    _check_decode(bsa, q, cache, lens, None)
+    idx = np.full((B, Hkv, keep), -1, np.int32)
+    for b, n in enumerate(lens):
+        own = -(-n // 64)
+        for g in range(Hkv):
+            kept = np.sort(r.permutation(own)[:keep])
+            idx[b, g, :len(kept)] = kept
+    _check_decode(bsa, q, cache, lens, idx)
+
+
+@pytest.mark.parametrize("G", [2, 16])
+def test_decode_of_the_largest_batch(bsa, G):
+    lens = [0] * 8192
+    for b in range(0, 8192, 37):
+        lens[b] = 1 + b % 100
+    lens[8191] = 128
+    q = torch.randn((8192, G, 64), generator=torch.Generator().manual_seed(G)).bfloat16()
+    _check_decode(bsa, q, _cache(lens, 1, 64, 2), lens, None)
+
+
 @pytest.mark.parametrize("spread,gain", [(0.0, 30.0), (12.0, 1.0), (0.0, 0.0), (4.0, 1e-30), (3.0, 1e4)])
 def test_decode_steep_flat_and_uneven_rows(bsa, spread, gain):
     # large logits, exponents far apart (values 2^12 apart and more), zero and tiny queries
@@ -585,6 +613,42 @@ def test_select_by_length(bsa, ncols):
         assert np.array_equal(count.cpu().numpy(), cnt)
         if max(lens) > ncols * 64:       # 65 tokens where the row has one column: taken as one block, and flagged
             _flagged(bsa)
+
+
+@pytest.mark.parametrize("ncols", [40, 1000, 5000])
+def test_select_by_length_of_close_tiny_and_huge_scores(bsa, ncols):
+    """Scores that differ in their last bits, subnormals, both zeros, the largest and infinite ones, and many equal to
+    the threshold: the order is the full fp32 one."""
+    r = np.random.default_rng(ncols)
+    tiny = np.float32(2.0 ** -149)
+    rows = [np.float32(1.5) + np.arange(ncols, dtype=np.float32) % 7 * np.float32(2.0 ** -23),
+            r.integers(-3, 4, ncols).astype(np.float32) * tiny,
+            np.where(r.random(ncols) < 0.5, np.float32(-0.0), np.float32(0.0)),
+            r.choice(np.array([np.inf, -np.inf, np.nan, 3.4e38, -3.4e38, 3.3e38, 1.0], np.float32), ncols),
+            -np.exp(r.standard_normal(ncols) * 20).astype(np.float32),
+            r.standard_normal(ncols).astype(np.float32),
+            np.full(ncols, np.nan, np.float32),
+            (r.integers(0, 2, ncols) * 2.0 ** -20 + 1).astype(np.float32)]
+    s = np.stack([row[r.permutation(ncols)] for row in rows])
+    lens = [64 * ncols] * len(rows)
+    for kb in (1, 5, ncols // 3, ncols - 2):
+        want, cnt = plain.select(s, lens, 1, 64, kb, kb + 1)
+        idx = torch.full((len(rows), kb + 1), -7, dtype=torch.int32, device="cuda")
+        count = torch.full((len(rows),), -7, dtype=torch.int32, device="cuda")
+        bsa.bsa_topk_select_lens(torch.from_numpy(s).cuda(), len(rows), ncols,
+                                 torch.tensor(lens, dtype=torch.int32).cuda(), 1, 64, kb, idx, kb + 1, count)
+        for row in range(len(rows)):
+            assert np.array_equal(idx[row].cpu().numpy(), want[row]), (ncols, kb, row)
+        assert np.array_equal(count.cpu().numpy(), cnt)
+
+
+def test_select_by_length_of_rows_at_an_odd_address(bsa):
+    base = torch.randn(4 * 300 + 1, generator=torch.Generator().manual_seed(1)).cuda()
+    s = base[1:].view(4, 300)
+    idx = torch.zeros((4, 9), dtype=torch.int32, device="cuda")
+    bsa.bsa_topk_select_lens(s, 4, 300, torch.tensor([300 * 64, 5000], dtype=torch.int32).cuda(), 2, 64, 8, idx, 9)
+    want, _ = plain.select(s.cpu().numpy(), [300 * 64, 5000], 2, 64, 8, 9)
+    assert np.array_equal(idx.cpu().numpy(), want)
 
 
 def test_select_by_length_flags_what_the_table_cannot_hold(bsa):
@@ -799,6 +863,20 @@ def test_binding_refuses_wrong_types(bsa, pipe):
         pipe.QuantDecodeStep(q, codes, codes, exps, exps, table, lens.long()).run()
     with pytest.raises(ValueError):
         pipe.QuantDecodeStep(q, codes, codes, exps, exps.int(), table, lens).run()
+    every = pipe.QuantDecodeStep(q, codes, codes.clone(), exps, exps.clone(), table, lens)
+    with pytest.raises(ValueError):
+        every.select()
+    with pytest.raises(ValueError):
+        every.attend(idx=torch.zeros((2, 2, 1), dtype=torch.int32, device="cuda"))
+    k = torch.zeros((1, 2, 3, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        every.append(k, k, new_lens=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        every.append(k.transpose(1, 2), k.transpose(1, 2))
+    with pytest.raises(ValueError):
+        every.append(k.float(), k.float())
+    with pytest.raises(ValueError):
+        every.read(k, k.clone(), starts=torch.zeros(2, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         pipe.QkvStep(torch.zeros((1, 2, 4, 64), device="cuda"), 2, 1, q_weight=torch.ones(64).bfloat16().cuda(),
                      k_weight=torch.ones(64).cuda()).run()

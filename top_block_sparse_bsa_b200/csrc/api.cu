@@ -1026,7 +1026,8 @@ bsa_status_t bsa_sparse_attn_decode_quant(const bsa_shape_t* s, const void* q, c
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return BSA_ERR_INVALID_ARG;
   if (s->dtype != BSA_BF16 || (s->d != 64 && s->d != 128) || s->Hq / s->Hkv > 16 || s->B > 8192)
     return BSA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(s->B) * (idx ? idx_stride : nb) >= (1ll << 31)) return BSA_ERR_UNSUPPORTED;
+  // list positions are counted in 32 bits, four 16-key pieces each
+  if (static_cast<int64_t>(s->B) * (idx ? idx_stride : nb) >= (1ll << 29)) return BSA_ERR_UNSUPPORTED;
   QuantDecodeArgs a{};
   int sms = 0;
   if ((st = device_state(&a.status, &sms)) != BSA_OK) return st;

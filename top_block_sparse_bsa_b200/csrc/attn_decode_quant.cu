@@ -632,23 +632,22 @@ cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t st) {
 
 }  // namespace qdecode
 
-// Groups of up to 8 heads are bound by memory, and 7/8 of the multiprocessors
-// draw more from it than all (the whole cache of 16 sequences, us: 148 blocks
-// 397, 132 389, 128 371, 120 372, 96 431; bytes in flight do not change it);
-// larger groups are bound by their products and take all (424 us, 487 with
-// 128).  Teams are halved, twice at most, until there are as many as rows.
+// One team of all warps an SM, or, while there are more rows than teams, two or
+// four smaller ones.  All multiprocessors take part: in short bursts 7/8 of them
+// draw more from memory than all (the whole cache of 16 sequences 371 us against
+// 397), but under steady load, where the power cap lowers the clock, they fall
+// behind (430 us against 405).
 // Ranges that end where rows end leave fewer records to join (97 kept blocks,
-// us: 128 rows on 128 ranges 40.2, on 148 42.7; 24 rows on 144 16.0, on 148
+// us: 128 rows on 128 ranges 42.3, on 148 45.0; 24 rows on 144 16.0, on 148
 // 19.0): from a list, where rows are equally long, as many ranges a row as fit
 // the teams, or whole rows a range, if that keeps at least 4/5 of the teams busy;
 // without one only where a row has four ranges or more (its own length may be
 // the only one).
 QuantSplit quant_decode_split(int num_sms, int group, int rows, bool list, int forced) {
   const int NB = group > 8 ? 2 : 1;
-  const int most = NB == 2 || num_sms < 2 ? num_sms : num_sms * 7 / 8;
   QuantSplit s;
   s.team_warps = qdecode::warps(NB);
-  int teams = most;
+  int teams = num_sms;
   if (forced > 0) {
     s.ranges = forced;
     s.ctas = forced;
@@ -662,7 +661,7 @@ QuantSplit quant_decode_split(int num_sms, int group, int rows, bool list, int f
   const int each = (rows + teams - 1) / teams;          // rows a range, where there are more rows than teams
   const int even = rows <= teams ? rows * (teams / rows) : (rows + each - 1) / each;
   if (5 * even >= 4 * teams && (list || rows <= teams / 4)) s.ranges = even;
-  s.ctas = s.ranges < most ? s.ranges : most;
+  s.ctas = s.ranges < num_sms ? s.ranges : num_sms;
   return s;
 }
 

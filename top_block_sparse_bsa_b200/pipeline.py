@@ -498,6 +498,8 @@ class QuantDecodeStep:
         s = self.shape
         if k_new.shape != v_new.shape or k_new.shape[:2] != (s.B, s.Hkv) or k_new.shape[3] != s.d:
             raise ValueError(f"new keys and values are [{s.B}, {s.Hkv}, T, {s.d}], got {list(k_new.shape)}")
+        if new_lens is not None and new_lens.shape != (s.B,):
+            raise ValueError(f"new_lens is [{s.B}], got {list(new_lens.shape)}")
         bsa_paged_append_quant(self._rows_shape(k_new.shape[2], k_new.dtype), k_new, v_new, self.seq_lens,
                                self.block_table, self.k_pool, self.v_pool, self.k_exp, self.v_exp,
                                self.bufs.get("kbar"), new_lens=new_lens, stream=stream)
@@ -507,10 +509,14 @@ class QuantDecodeStep:
         s = self.shape
         if k_out.shape != v_out.shape or k_out.shape[:2] != (s.B, s.Hkv) or k_out.shape[3] != s.d:
             raise ValueError(f"rows read back are [{s.B}, {s.Hkv}, T, {s.d}], got {list(k_out.shape)}")
+        if starts is not None and starts.shape != (s.B,):
+            raise ValueError(f"starts is [{s.B}], got {list(starts.shape)}")
         bsa_paged_read_quant(self._rows_shape(k_out.shape[2], k_out.dtype), self.k_pool, self.v_pool, self.k_exp,
                              self.v_exp, self.block_table, self.seq_lens, k_out, v_out, starts=starts, stream=stream)
 
     def select(self, stream=None):
+        if self.kb is None:
+            raise ValueError("this step attends every block (kb None): there is nothing to select")
         b, s = self.bufs, self.shape
         bsa_score_blocks(s, BSA_SCORE_DECODE, self.q, None, b["kbar"], b["qbar"], None, b["scores"], stream=stream)
         bsa_topk_select_lens(b["scores"], s.B * s.Hkv, self.nb, self.seq_lens, s.Hkv, self.block, self.kb, b["idx"],
@@ -518,7 +524,10 @@ class QuantDecodeStep:
 
     def attend(self, idx: Optional[torch.Tensor] = None, stream=None, with_lse: bool = True):
         b = self.bufs
-        idx = b.get("idx") if idx is None else idx
+        if idx is None:
+            idx = b.get("idx")
+        elif idx.dim() != 3 or idx.shape[0] != self.shape.B or idx.shape[1] != self.shape.Hkv:
+            raise ValueError(f"idx is [{self.shape.B}, {self.shape.Hkv}, n], got {list(idx.shape)}")
         bsa_sparse_attn_decode_quant(self.shape, self.q, self.k_pool, self.v_pool, self.k_exp, self.v_exp,
                                      self.block_table, self.seq_lens, idx, 0 if idx is None else idx.shape[-1],
                                      self.softmax_scale, b["workspace"], b["o"], b["lse"] if with_lse else None,
