@@ -183,7 +183,10 @@ def _dtype_code(t: torch.Tensor) -> int:
 def make_shape(B, Hq, Hkv, Nq, Nk, d, block, dtype) -> BsaShape:
     if isinstance(dtype, torch.dtype):
         dtype = BSA_BF16 if dtype == torch.bfloat16 else BSA_F32
-    return BsaShape(int(B), int(Hq), int(Hkv), int(Nq), int(Nk), int(d), int(block), int(dtype))
+    try:
+        return BsaShape(B, Hq, Hkv, Nq, Nk, d, block, dtype)
+    except TypeError:      # numbers that are no Python ints
+        return BsaShape(int(B), int(Hq), int(Hkv), int(Nq), int(Nk), int(d), int(block), int(dtype))
 
 
 def bsa_version() -> int:
