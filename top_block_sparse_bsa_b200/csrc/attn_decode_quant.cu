@@ -280,14 +280,18 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
       const int row = __shfl_sync(0xffffffffu, my_row, src);
       said = l_no * 32 + __shfl_sync(0xffffffffu, my_n, src);
       const uint32_t dst = ring_u32 + slot * SB;
-      const uint8_t* k = p.k_pool + static_cast<int64_t>(row) * (16 * D);
-      const uint8_t* v = p.v_pool + static_cast<int64_t>(row) * (16 * D);
-      constexpr int PR = D / 16;      // 16-byte pieces of a row
+      const uint8_t* k = p.k_pool + static_cast<int64_t>(row) * (16 * D) + lane * 16;
+      const uint8_t* v = p.v_pool + static_cast<int64_t>(row) * (16 * D) + lane * 16;
+      // 512 bytes a step, whole rows: the step changes the row by a multiple of 4, so the lane's place in it is fixed
+      // but for the values' swizzle, which takes bit 2 of the row
+      constexpr int PR = D / 16, kStep = 32 / PR;      // 16-byte pieces of a row, rows of a step
+      const int rr = lane / PR, q = lane % PR;
+      const uint32_t kd = dst + rr * D + (q ^ k_swizzle<D>(rr)) * 16;
+      const uint32_t vd0 = rr * D + (q ^ v_swizzle<D>(rr)) * 16, vd1 = rr * D + (q ^ v_swizzle<D>(rr + 4)) * 16;
 #pragma unroll
       for (int i = 0; i < PR / 2; ++i) {
-        const int e = i * 32 + lane, rr = e / PR, q = e % PR;
-        cp_async16(dst + rr * D + (q ^ k_swizzle<D>(rr)) * 16, k + e * 16);
-        cp_async16(dst + 16 * D + rr * D + (q ^ v_swizzle<D>(rr)) * 16, v + e * 16);
+        cp_async16(kd + i * 512, k + i * 512);
+        cp_async16(dst + 16 * D + i * 512 + ((i * kStep) & 4 ? vd1 : vd0), v + i * 512);
       }
       if (lane < 2) cp_async16(dst + 32 * D + lane * 16, (lane ? p.v_exp : p.k_exp) + static_cast<int64_t>(row) * 16);
     }
@@ -387,9 +391,9 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
       for (int i = 0; i < 2; ++i) {
         const int key = r + 8 * i;
         uint32_t ke = st[32 * D + key], ve = st[32 * D + 16 + key];
-        if (key >= n) ke = ve = 127u;
+        if (n < 16 && key >= n) ke = ve = 127u;     // may hold anything
         kf[i] = __uint_as_float(ke << 23);
-        vb[i] = static_cast<float>(static_cast<int>(ve) - 127);
+        vb[i] = __uint_as_float(0x4B000000u | ve) - 8388735.0f;      // ve - 127, through 2^23 + ve
         back[i] = __uint_as_float((254u - ve) << 23);
       }
       uint32_t wb[NB][2];
@@ -401,8 +405,8 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float v = S[nb][2 * i + h] * kf[i] * qs[nb][h] + vb[i];
-            y[2 * i + h] = r + 8 * i < n ? v : -INFINITY;
+            y[2 * i + h] = S[nb][2 * i + h] * kf[i] * qs[nb][h] + vb[i];
+            if (n < 16 && r + 8 * i >= n) y[2 * i + h] = -INFINITY;
             high |= y[2 * i + h] > M[nb][h] + kHeadroom;
           }
         if (__any_sync(0xffffffffu, high)) {
@@ -448,10 +452,14 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
           const uint2 t = *reinterpret_cast<const uint2*>(src + ((r >> 1) ^ v_swizzle<D>(row)) * 16 + (r & 1) * 8);
           vr[i][0] = t.x, vr[i][1] = t.y;
         }
-        if (row >= n) {   // rows past the sequence may hold anything: a zero weight does not silence a NaN
+      }
+      if (n < 16) {   // rows past the sequence may hold anything: a zero weight does not silence a NaN
 #pragma unroll
-          for (int k = 0; k < VW; ++k) vr[i][k] = 0u;
-        }
+        for (int i = 0; i < 4; ++i)
+          if (2 * c + (i & 1) + 8 * (i >> 1) >= n) {
+#pragma unroll
+            for (int k = 0; k < VW; ++k) vr[i][k] = 0u;
+          }
       }
 #pragma unroll
       for (int k = 0; k < VW; ++k) {
