@@ -443,9 +443,11 @@ def test_decode_with_other_splits(bsa, splits):
         bsa.bsa_decode_split_override(prev)
 
 
-@pytest.mark.parametrize("B,Hkv,G", [(20, 8, 4), (40, 8, 1), (80, 8, 3), (20, 8, 12), (40, 8, 16)])
+@pytest.mark.parametrize("B,Hkv,G", [(20, 8, 4), (40, 8, 1), (80, 8, 3), (20, 8, 12), (40, 8, 16),
+                                     (16, 8, 4), (30, 8, 2), (64, 8, 1), (16, 8, 9), (64, 8, 10)])
 def test_decode_of_many_rows(bsa, B, Hkv, G):
-    """More rows than multiprocessors: blocks of threads split into teams, ranges with several rows each."""
+    """About as many rows as multiprocessors, and more: blocks of threads split into teams, ranges that hold whole rows
+    (then one launch writes every output, those of rows without a block too), ranges with several rows each."""
     r = np.random.default_rng(B + G)
     lens = r.integers(0, 260, B).tolist()
     nb, keep = 5, 3
@@ -458,6 +460,8 @@ def test_decode_of_many_rows(bsa, B, Hkv, G):
         for g in range(Hkv):
             kept = np.sort(r.permutation(own)[:keep])
             idx[b, g, :len(kept)] = kept
+    idx[1, 0] = -1
+    idx[2, 1] = [-1, -2 ** 31, -1]
     _check_decode(bsa, q, cache, lens, idx)
 
 

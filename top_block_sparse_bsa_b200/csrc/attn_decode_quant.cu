@@ -13,20 +13,19 @@
 // for each of at most 16 heads; the cache's own bytes, read once per KV head
 // for all its query heads, are the floor.  So the design keeps loads in
 // flight and spends few instructions a byte:
-//   - a warp takes 16 keys at a time, straight from memory into registers as
-//     16-byte pieces: no shared-memory stage, no barrier, no block-wide wait in
-//     the loop.  The next 16 keys are loaded while these keys' weights and
-//     product are formed, the next values behind them.
+//   - a warp takes 16 keys at a time through stages of its own: asynchronous
+//     copies bring 4 KB two to six chunks ahead and run on across the rows of
+//     its range; no barrier and no block-wide wait stands in the loop.
 //   - the codes become fp16 pairs by one conversion each (exact), and the
 //     products run on m16n8k16 matrix instructions with the keys (then the
 //     channels) as the 16 rows and eight query heads as the 8 columns.  The
 //     order of the contracted index is free as long as both operands agree,
-//     so each lane's share is whatever its 16-byte loads bring: channels for
+//     so each lane's share is what 16-byte reads of a stage bring: channels for
 //     q . K; for V, lanes pair two keys' bytes and number the channels as they
 //     hold them.  Tensor-memory instructions would need the codes split from
 //     their rows' exponents across lanes and a block-wide exchange of maxima
 //     for every 128 keys, at twice the keys a second of the bf16 kernel, for
-//     a part that is not the bound.
+//     a part that is not the bound: the matrix unit is 20% busy.
 //   - M moves only when some y passes it by 2^7 (one vote a step; M starts at
 //     the first maximum): w is scaled by 2^8, so it stays within fp16 and keeps
 //     its 11 bits down to 2^-22 of the largest.
@@ -40,6 +39,10 @@
 // it joins its warps.  A range that holds a whole row writes its output; a row
 // cut by range borders leaves one partial record (M, l, O) per range, at most
 // two a team, and the second kernel joins them.
+//
+// 16 ragged sequences of 8 KV heads, 32 query heads: every block (2.5 GB) 382 to
+// 405 us (92 to 98% of the copy rate, by the clock under the power cap), 97 kept
+// blocks 39.6 us (79%); one sequence of 4001 tokens 10 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
       if (u < 4 * (li.t1 - li.t0)) {
         const int t = li.t0 + (u >> 2);
         const int blk = p.idx ? __ldg(p.idx + (static_cast<int64_t>(li.b) * p.Hkv + li.g) * p.list_len + t) : t;
-        const int pos = blk * 64 + (u & 3) * 16;
+        const int pos = max(min(blk, p.nb), -1) * 64 + (u & 3) * 16;
         if (blk >= p.nb) {
           atomicOr(p.status, BSA_DEV_BAD_INDEX);
         } else if (blk >= 0 && pos < l_len) {
