@@ -555,7 +555,8 @@ bsa_status_t bsa_paged_read_quant(const bsa_shape_t* shape, const void* k_pool, 
  *   own length has no keys; an entry >= nb, or a needed table entry outside
  *   [0, num_pages), is skipped and flagged (BSA_DEV_BAD_INDEX).
  * o [B,Hq,d] bf16; lse [B,Hq] fp32 (optional), natural log.  A row without a
- *   key gives o = 0 and lse = -inf.
+ *   key gives o = 0 and lse = -inf.  Value rows whose exponent byte is below 56
+ *   (values under 2^-62) enter o with an absolute error of up to 2^-94.
  * workspace: bsa_workspace_bytes(BSA_OP_DECODE_QUANT, shape, idx_stride) bytes,
  *   256-byte aligned; its contents on entry do not matter; calls that may
  *   overlap need one each.

@@ -369,7 +369,7 @@ def _cache(lens, Hkv, d, nb, seed=0, spread=1.0):
     return pools[0], pools[1], exps[0], exps[1], table
 
 
-def _check_decode(bsa, q, cache, lens, idx, scale=None, what=""):
+def _check_decode(bsa, q, cache, lens, idx, scale=None, what="", far=0.0):
     B, Hq, d = q.shape
     k, v, ke, ve, table = cache
     Hkv, nb = k.shape[1], table.shape[1]
@@ -389,7 +389,7 @@ def _check_decode(bsa, q, cache, lens, idx, scale=None, what=""):
     # a logit is a sum of d products in fp32, d 2^-24 of the products' sizes (taken whole, whichever way the matrix
     # unit adds); a weight moves by that, its fp16 rounding (2^-11) and the exponential (2^-22); the output is rounded
     # once more
-    off = size * d * 2.0 ** -24 * 2 + 2.0 ** -20
+    off = size * d * 2.0 ** -24 * 2 + 2.0 ** -20 + far
     tol = HALF[torch.bfloat16] * np.abs(want) + (2.0 ** -11 + 2 * off)[..., None] * 1.01 * weight
     err = np.abs(got - want)
     assert np.all(err <= tol), (what, np.unravel_index(np.argmax(err - tol), err.shape), (err - tol).max())
@@ -482,6 +482,28 @@ def test_decode_steep_flat_and_uneven_rows(bsa, spread, gain):
     q = (gain * torch.randn((2, 4, 128), generator=torch.Generator().manual_seed(6))).bfloat16()
     _check_decode(bsa, q, _cache(lens, 1, 128, 9, seed=3, spread=spread), lens, None,
                   scale=1 / math.sqrt(128) / max(1.0, gain / 30) / 2.0 ** (2 * spread))
+
+
+@pytest.mark.parametrize("zeros", ["all", "before", "behind", "between", "one"])
+@pytest.mark.parametrize("e_rest", [60, 119, 165, 240])
+def test_decode_with_rows_of_zero_values(bsa, zeros, e_rest):
+    """A value row of zeros (exponent 10) has the weight of its logit, whatever stands beside it: in long runs before,
+    behind or between other rows, whose exponents differ from its own by up to 230."""
+    lens = [2500, 40, 700]
+    cache = _cache(lens, 1, 128, 40, seed=5)
+    r = np.random.default_rng(5)
+    for b, n in enumerate(lens):
+        t = np.arange(n)
+        off = {"all": t >= 0, "before": t < n - 3, "behind": t > 2, "between": r.random(n) < 0.5, "one": t == n // 2}[zeros]
+        page = cache[4][b, t // 64]
+        cache[1][page[off], 0, t[off] % 64] = 0
+        cache[3][page, 0, t % 64] = np.where(off, 10, e_rest)
+    q = torch.randn((3, 8, 128), generator=torch.Generator().manual_seed(8)).bfloat16()
+    # a logit against the reference, up to 128 octaves away: a rounding of 2^-18 octaves, three of them
+    _check_decode(bsa, q, cache, lens, None, scale=0.02, far=3 * 2.0 ** -18)
+    idx = np.full((3, 1, 4), -1, np.int32)
+    idx[0, 0], idx[1, 0, :1], idx[2, 0, :3] = [0, 7, 38, 39], [0], [0, 5, 10]
+    _check_decode(bsa, q, cache, lens, idx, scale=0.02, far=3 * 2.0 ** -18)
 
 
 def test_decode_ascending_logits_move_the_reference(bsa):

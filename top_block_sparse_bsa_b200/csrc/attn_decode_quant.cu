@@ -5,7 +5,7 @@
 // Formula.  A key is K_t 2^a_t, a value V_t 2^b_t (K, V rows of e4m3 codes,
 // a, b the row's exponents).  With x_t = (q . K_t) 2^a_t scale log2(e) and
 // y_t = x_t + b_t, any reference M >= about max y:
-//   w_t = 2^(y_t - M),  O = sum w_t V_t,  l = sum w_t 2^-b_t,  o = O / l,
+//   w_t = 2^(y_t - M),  O = sum w_t V_t,  l = sum 2^(x_t - M),  o = O / l,
 // so the value's exponent rides in the softmax weight and the matrix product
 // takes the codes as they are.  lse = ln2 (M + log2 l).
 //
@@ -29,7 +29,7 @@
 //   - M moves only when some y passes it by 2^7 (one vote a step; M starts at
 //     the first maximum): w is scaled by 2^8, so it stays within fp16 and keeps
 //     its 11 bits down to 2^-22 of the largest.
-// w is rounded to fp16 for the product (at most 2^-11 of w); l sums it in fp32
+// w is rounded to fp16 for the product (at most 2^-11 of w); l sums its terms
 // unrounded; logits, O and l are fp32.
 //
 // Work split: the rows' list positions are laid end to end, each sequence
@@ -53,6 +53,14 @@ namespace qdecode {
 
 constexpr float kLift = 8.0f;        // weights are 2^(y - M + 8)
 constexpr float kHeadroom = 7.0f;    // M moves when y > M + 7: weights stay below 2^15
+// A key's term of l is u = 2^(x - M + 8 + 16) and its weight u 2^(b - 16): with the
+// 16, u stays normal 31 octaves below its largest for any b.  For M an exponent
+// byte counts as at least 56, so u is at most 2^102 and 2^25 of them stay finite,
+// whatever rows of zeros (byte 10) stand before others.  Rows below 56 (values
+// under 2^-62) weigh less than M would let them, down to fp16's subnormals: an
+// error of o under 2^-94, absolute.
+constexpr int kDeep = 16;
+constexpr uint32_t kLeastExp = 56u;
 
 // NB = sets of eight query heads a warp carries; one block an SM: 16 warps of
 // two stages (three stages: 97 kept blocks x 16 sequences 41.6 us against 40.2),
@@ -389,15 +397,15 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
         }
       }
       // ---- weights
-      float kf[2], vb[2], back[2];
+      float kf[2], vf[2], vb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int key = r + 8 * i;
         uint32_t ke = st[32 * D + key], ve = st[32 * D + 16 + key];
         if (n < 16 && key >= n) ke = ve = 127u;     // may hold anything
         kf[i] = __uint_as_float(ke << 23);
-        vb[i] = __uint_as_float(0x4B000000u | ve) - 8388735.0f;      // ve - 127, through 2^23 + ve
-        back[i] = __uint_as_float((254u - ve) << 23);
+        vf[i] = __uint_as_float((max(ve, static_cast<uint32_t>(kDeep)) - kDeep) << 23);
+        vb[i] = __uint_as_float(0x4B000000u | max(ve, kLeastExp)) - 8388735.0f;      // - 127, through 2^23
       }
       uint32_t wb[NB][2];
 #pragma unroll
@@ -408,20 +416,21 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            y[2 * i + h] = S[nb][2 * i + h] * kf[i] * qs[nb][h] + vb[i];
+            y[2 * i + h] = S[nb][2 * i + h] * kf[i] * qs[nb][h];
             if (n < 16 && r + 8 * i >= n) y[2 * i + h] = -INFINITY;
-            high |= y[2 * i + h] > M[nb][h] + kHeadroom;
+            high |= y[2 * i + h] + vb[i] > M[nb][h] + kHeadroom;
           }
         if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float t = fmaxf(y[h], y[2 + h]);
+            float t = fmaxf(y[h] + vb[0], y[2 + h] + vb[1]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
             const float m_new = fmaxf(M[nb][h], t);
-            const float a = (m_new == -INFINITY) ? 1.0f : fast_exp2(M[nb][h] - m_new);
+            const float root = (m_new == -INFINITY) ? 1.0f : fast_exp2(0.5f * (M[nb][h] - m_new));
             M[nb][h] = m_new;
-            l[nb][h] *= a;
+            l[nb][h] = l[nb][h] * root * root;
+            const float a = root * root;
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
               O[nb][m][h] *= a;
@@ -432,11 +441,12 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
         float wgt[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float ref = (M[nb][h] == -INFINITY) ? 0.0f : kLift - M[nb][h];
+          const float ref = (M[nb][h] == -INFINITY) ? 0.0f : kLift + kDeep - M[nb][h];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            wgt[2 * i + h] = fast_exp2(y[2 * i + h] + ref);
-            l[nb][h] += wgt[2 * i + h] * back[i];
+            const float u = fast_exp2(y[2 * i + h] + ref);
+            l[nb][h] += u;
+            wgt[2 * i + h] = u * vf[i];
           }
         }
         // keys x heads -> heads x keys: the B operand of O^T = V^T w
@@ -522,18 +532,18 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
         for (int k = w0; k < w0 + team_warps; ++k) {
           const float mk = sm_m[k][nb * 8 + h];
           if (mk == -INFINITY) continue;      // a warp without a key: it may have no spare stage
-          const float f = fast_exp2(mk - mx);
+          const float root = fast_exp2(0.5f * (mk - mx)), f = root * root;
           const float2 v = reinterpret_cast<const float2*>(smem_raw + (k * R + sm_slot[k]) * SB)[at];
-          L += f * sm_l[k][nb * 8 + h];
+          L += root * sm_l[k][nb * 8 + h] * root;
           o0 += f * v.x;
           o1 += f * v.y;
         }
         const int64_t orow = static_cast<int64_t>(b) * p.Hq + it.g * G + nb * 8 + h;
         if (whole) {
-          const float inv = (mx == -INFINITY) ? 0.0f : 1.0f / L;
+          const float inv = (mx == -INFINITY) ? 0.0f : static_cast<float>(1 << kDeep) / L;
           reinterpret_cast<uint32_t*>(p.o + orow * D)[pr] = pack_bf16x2(o0 * inv, o1 * inv);
           if (p.lse && pr == 0)
-            p.lse[orow] = (mx == -INFINITY) ? -INFINITY : (mx - kLift + log2f(L)) * 0.69314718055994530942f;
+            p.lse[orow] = (mx == -INFINITY) ? -INFINITY : (mx - (kLift + kDeep) + log2f(L)) * 0.69314718055994530942f;
         } else {
           float* rec = p.partial + ((static_cast<int64_t>(range) * 2 + slot) * G + nb * 8 + h) * (D + 4);
           *reinterpret_cast<float2*>(rec + 4 + 2 * pr) = make_float2(o0, o1);
@@ -593,14 +603,14 @@ __global__ void __launch_bounds__(D * PARTS) combine_kernel(const QuantDecodeArg
 #pragma unroll
     for (int i = 0; i < 8; ++i) m_new = fmaxf(m_new, ml[i].x);
     if (m_new == -INFINITY) continue;
-    const float a = exp2f(M - m_new);
-    L *= a;
-    acc *= a;
+    const float root = exp2f(0.5f * (M - m_new));
+    L = L * root * root;
+    acc *= root * root;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float f = exp2f(ml[i].x - m_new);     // 0 where the record is empty
-      L += f * ml[i].y;
-      acc += f * o[i];
+      const float f = exp2f(0.5f * (ml[i].x - m_new));     // 0 where the record is empty
+      L += f * ml[i].y * f;
+      acc += f * f * o[i];
     }
     M = m_new;
   }
@@ -618,14 +628,14 @@ __global__ void __launch_bounds__(D * PARTS) combine_kernel(const QuantDecodeArg
     if (M != -INFINITY) {
 #pragma unroll
       for (int k = 0; k < PARTS; ++k) {
-        const float f = exp2f(part_m[k] - M);
-        L += f * part_l[k];
-        acc += f * part_o[k][ch];
+        const float f = exp2f(0.5f * (part_m[k] - M));
+        L += f * part_l[k] * f;
+        acc += f * f * part_o[k][ch];
       }
     }
   }
-  p.o[orow * D + ch] = __float2bfloat16_rn(M == -INFINITY ? 0.0f : acc / L);
-  if (p.lse && ch == 0) p.lse[orow] = (M == -INFINITY) ? -INFINITY : (M - kLift + log2f(L)) * 0.69314718055994530942f;
+  p.o[orow * D + ch] = __float2bfloat16_rn(M == -INFINITY ? 0.0f : acc * (static_cast<float>(1 << kDeep) / L));
+  if (p.lse && ch == 0) p.lse[orow] = (M == -INFINITY) ? -INFINITY : (M - (kLift + kDeep) + log2f(L)) * 0.69314718055994530942f;
 }
 
 template <int D, int NB>
