@@ -91,6 +91,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -358,11 +363,12 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
       qs[nb][1] = __shfl_sync(0xffffffffu, down, (2 * c + 1) * 4);
     }
 
-    float M[NB][2], l[NB][2], O[NB][MB][4];
+    float M[NB][2], O[NB][MB][4];
+    uint64_t l[NB];        // of two heads
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       M[nb][0] = M[nb][1] = -INFINITY;
-      l[nb][0] = l[nb][1] = 0.0f;
+      l[nb] = 0ull;
 #pragma unroll
       for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -410,26 +416,30 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
       uint32_t wb[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float y[4];
+        uint64_t yy[2];        // a key's logits of two heads
         bool high = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            y[2 * i + h] = S[nb][2 * i + h] * kf[i] * qs[nb][h];
-            if (n < 16 && r + 8 * i >= n) y[2 * i + h] = -INFINITY;
-            high |= y[2 * i + h] + vb[i] > M[nb][h] + kHeadroom;
-          }
+        for (int i = 0; i < 2; ++i) {
+          yy[i] = f2_mul(f2_mul(f2_pack(S[nb][2 * i], S[nb][2 * i + 1]), f2_pack(kf[i], kf[i])), f2_pack(qs[nb][0], qs[nb][1]));
+          if (n < 16 && r + 8 * i >= n) yy[i] = f2_pack(-INFINITY, -INFINITY);
+          float y0, y1;
+          f2_unpack(f2_add(yy[i], f2_pack(vb[i], vb[i])), y0, y1);
+          high |= y0 > M[nb][0] + kHeadroom || y1 > M[nb][1] + kHeadroom;
+        }
         if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float t = fmaxf(y[h] + vb[0], y[2 + h] + vb[1]);
+            float ya[2], yb[2];
+            f2_unpack(yy[0], ya[0], ya[1]);
+            f2_unpack(yy[1], yb[0], yb[1]);
+            float t = fmaxf(ya[h] + vb[0], yb[h] + vb[1]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
             const float m_new = fmaxf(M[nb][h], t);
             const float root = (m_new == -INFINITY) ? 1.0f : fast_exp2(0.5f * (M[nb][h] - m_new));
             M[nb][h] = m_new;
-            l[nb][h] = l[nb][h] * root * root;
+            const uint64_t rr = h ? f2_pack(1.0f, root) : f2_pack(root, 1.0f);
+            l[nb] = f2_mul(f2_mul(l[nb], rr), rr);
             const float a = root * root;
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
@@ -438,16 +448,16 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
             }
           }
         }
+        const float ref0 = (M[nb][0] == -INFINITY) ? 0.0f : kLift + kDeep - M[nb][0];
+        const float ref1 = (M[nb][1] == -INFINITY) ? 0.0f : kLift + kDeep - M[nb][1];
         float wgt[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float ref = (M[nb][h] == -INFINITY) ? 0.0f : kLift + kDeep - M[nb][h];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float u = fast_exp2(y[2 * i + h] + ref);
-            l[nb][h] += u;
-            wgt[2 * i + h] = u * vf[i];
-          }
+        for (int i = 0; i < 2; ++i) {
+          float e0, e1;
+          f2_unpack(f2_add(yy[i], f2_pack(ref0, ref1)), e0, e1);
+          const uint64_t u = f2_pack(fast_exp2(e0), fast_exp2(e1));
+          l[nb] = f2_add(l[nb], u);
+          f2_unpack(f2_mul(u, f2_pack(vf[i], vf[i])), wgt[2 * i], wgt[2 * i + 1]);
         }
         // keys x heads -> heads x keys: the B operand of O^T = V^T w
         wb[nb][0] = transpose8x8(pack_f16x2(wgt[0], wgt[1]));
@@ -495,15 +505,17 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
     // ---- join the warps, then write the row or its partial record; a warp's O waits in its spare stage
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
+      float ls[2];
+      f2_unpack(l[nb], ls[0], ls[1]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l[nb][h] += __shfl_xor_sync(0xffffffffu, l[nb][h], o);
+        for (int o = 4; o < 32; o <<= 1) ls[h] += __shfl_xor_sync(0xffffffffu, ls[h], o);
         // a NaN logit leaves M as it is; without another key the row must still not pass for an empty one
-        if (M[nb][h] == -INFINITY && l[nb][h] != l[nb][h]) M[nb][h] = 0.0f;
+        if (M[nb][h] == -INFINITY && ls[h] != ls[h]) M[nb][h] = 0.0f;
         if (r == 0) {
           sm_m[warp][nb * 8 + 2 * c + h] = M[nb][h];
-          sm_l[warp][nb * 8 + 2 * c + h] = l[nb][h];
+          sm_l[warp][nb * 8 + 2 * c + h] = ls[h];
         }
       }
     }
