@@ -462,7 +462,8 @@ bsa_status_t bsa_rope_inv_freq(int rot_dim, double base, int scaling, double fac
  *   token_stride >= (Hq + 2 Hkv) d (a slice of a wider projection may be
  *   passed), its bytes a multiple of 16.
  * q_weight, k_weight [d] (dtype): y = x / sqrt(mean(x^2) + eps) * weight.
- *   Both or neither; NULL: no norm.  eps >= 0.
+ *   Both or neither; NULL: no norm.  eps >= 0.  The mean of squares is fp32: a
+ *   row of magnitudes past 2^60 or so, or under 2^-60 with eps 0, is out of range.
  * rope: see bsa_rope_t; NULL or BSA_ROPE_NONE: no rotation.
  * positions [B, Nq] int32 (optional): the tokens' positions, any int32; NULL:
  *   0..Nq-1.  Angles are formed to 2^-32 turns at any position.
@@ -480,7 +481,8 @@ bsa_status_t bsa_qkv_norm_rope(const bsa_shape_t* shape, const void* qkv, long l
  * of the weights.
  * Inputs: the forward's, and dq [B,Hq,Nq,d], dk and dv [B,Hkv,Nq,d] fp32.
  * d_qkv: laid out as qkv with d_token_stride; dtype, rounded once; every head's
- *   channels are written, elements between tokens are left as they are.
+ *   channels are written, elements between tokens are left as they are.  No
+ *   output may overlap an input.
  * d_q_weight, d_k_weight [d] fp32: written (not added to); required with
  *   weights, NULL without.  Sums run in a fixed order: equal inputs give equal
  *   bits.

@@ -187,6 +187,28 @@ def test_encode_backward(pipe, B, N, Hq, Hkv, d, rot, norm, layout, dtype):
         assert all(torch.equal(again[n], got[n]) for n in again)
 
 
+@pytest.mark.parametrize("exponent", [-45, -20, 30])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_encode_and_backward_of_tiny_and_large_rows_without_eps(pipe, exponent, dtype):
+    # the norm does not see a factor on a row; its gradient is divided by it (2^45: the cube of 1/rms leaves fp32)
+    qkv = _qkv(1, 21, 4, 2, 128, dtype, spread=0.0) * 2.0 ** exponent
+    w = _weights(128, dtype, True)
+    freq, _ = _rope_inputs(128, "half")
+    g = torch.Generator().manual_seed(4)
+    grads = [torch.randn((1, h, 21, 128), generator=g) for h in (4, 2, 2)]
+    step = _encode_step(pipe, qkv.cuda(), 4, 2, w, freq, "half", None, 1.0, eps=0.0)
+    out = step.run()
+    wd = [x.double() for x in w]
+    for name, x in zip(("q", "k"), plain.encode(qkv.double(), 4, 2, *wd, 0.0, freq, "half", None, 1.0)[:2]):
+        top = x.abs().amax(-1, keepdim=True) * 2
+        assert bool(((out[name].cpu().double() - x).abs() <= HALF[dtype] * x.abs() + 2.0 ** -19 * top).all()), name
+    got = step.backward(*(x.cuda() for x in grads))
+    want, (size, _) = plain.encode_grad(qkv.double(), 4, 2, *wd, 0.0, freq, "half", None, 1.0,
+                                        *(x.double() for x in grads))
+    err = (got["d_qkv"].cpu().double() - want[0]).abs()
+    assert bool((err <= HALF[dtype] * want[0].abs() + 2.0 ** -18 * size).all()), (err / (size + 1e-30)).max()
+
+
 def test_encode_backward_agrees_with_differences_of_the_kernel(pipe):
     # fp32, a directional difference of the forward kernel itself
     B, N, Hq, Hkv, d = 1, 13, 4, 2, 64

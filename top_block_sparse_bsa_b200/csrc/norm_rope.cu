@@ -443,12 +443,12 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
             f2_unpack(ss, s0, s1);
             f2_unpack(sd, d0, d1);
             const float r = rsqrtf(row_sum<GS>(s0 + s1) * p.inv_d + p.eps);
-            const float k3 = -r * r * r * row_sum<GS>(d0 + d1) * p.inv_d;
-            const uint64_t rr = f2_pack(r, r), kk = f2_pack(k3, k3);
+            const float k2 = -r * (r * row_sum<GS>(d0 + d1)) * p.inv_d;      // r^3 may leave fp32, this only with r^2
+            const uint64_t rr = f2_pack(r, r), kk = f2_pack(k2, k2);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               dW[k] = f2_fma(t[k], rr, dW[k]);
-              dy[k] = f2_fma(x[k], kk, f2_mul(f2_mul(dy[k], W[k]), rr));
+              dy[k] = f2_mul(f2_fma(x[k], kk, f2_mul(dy[k], W[k])), rr);
             }
           }
           if (m.on && live && h0 + u < to) {
