@@ -27,6 +27,12 @@ namespace qcache {
 constexpr int kThreads = 256;          // reads
 constexpr int kAppendThreads = 128;
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Exponent byte of a row whose largest finite magnitude is m.
 __device__ __forceinline__ uint32_t exponent_byte(float m) {
   const uint32_t u = __float_as_uint(m);
@@ -59,16 +65,17 @@ __device__ __forceinline__ float amax3(float a, float b, float c) {
   return d;
 }
 template <int GS>
-__device__ __forceinline__ float group_amax(float m, uint32_t group_mask) {
+__device__ __forceinline__ float group_amax(float m) {
 #pragma unroll
-  for (int o = GS / 2; o; o >>= 1) m = amax2(m, __shfl_xor_sync(group_mask, m, o));
+  for (int o = GS / 2; o; o >>= 1) m = amax2(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
-// The codes of a lane's 8 W bf16 values and the row's exponent byte.
+// The codes of a lane's 8 W bf16 values and the row's exponent byte; called by
+// whole warps.  Rows with infinities or NaN take branches of their own: their
+// selects would cost every row a third of its instructions.
 template <int GS, int W>
-__device__ __forceinline__ void quantise_row(const uint4 (&x)[W], uint32_t group_mask, uint32_t (&code)[2 * W],
-                                             uint32_t& e) {
+__device__ __forceinline__ void quantise_row(const uint4 (&x)[W], uint32_t (&code)[2 * W], uint32_t& e) {
   float v[8 * W];
 #pragma unroll
   for (int k = 0; k < W; ++k) {
@@ -82,29 +89,33 @@ __device__ __forceinline__ void quantise_row(const uint4 (&x)[W], uint32_t group
   float m = amax2(v[0], v[1]);
 #pragma unroll
   for (int i = 2; i < 8 * W; i += 2) m = amax3(m, v[i], v[i + 1]);
-  m = group_amax<GS>(m, group_mask);
+  m = group_amax<GS>(m);
   const bool broken = !(m < INFINITY);      // the same for the whole row
-  if (broken) {
-    m = 0.0f;
+  const bool any_broken = __any_sync(0xffffffffu, broken);
+  if (any_broken) {
+    float f = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8 * W; ++i) m = fmaxf(m, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.0f);
-    m = group_amax<GS>(m, group_mask);
+    for (int i = 0; i < 8 * W; ++i) f = fmaxf(f, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.0f);
+    f = group_amax<GS>(f);
+    if (broken) m = f;
   }
   e = exponent_byte(m);
-  const float inv = two_to(254u - e);
+  const uint64_t inv = f2_pack(two_to(254u - e), two_to(254u - e));
 #pragma unroll
   for (int k = 0; k < 2 * W; ++k) {
     uint32_t two[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float lo = v[4 * k + 2 * i], hi = v[4 * k + 2 * i + 1];
-      two[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo * inv, hi * inv), __NV_SATFINITE, __NV_E4M3);
-      if (broken) {
-        if (!(fabsf(lo) < INFINITY)) two[i] = (two[i] & 0xFF00u) | 0x7Fu;
-        if (!(fabsf(hi) < INFINITY)) two[i] = (two[i] & 0x00FFu) | 0x7F00u;
-      }
+      float2 t;
+      f2_unpack(f2_mul(f2_pack(v[4 * k + 2 * i], v[4 * k + 2 * i + 1]), inv), t.x, t.y);
+      two[i] = __nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3);
     }
     code[k] = two[0] | (two[1] << 16);
+  }
+  if (any_broken) {      // a conversion saturates infinities
+#pragma unroll
+    for (int i = 0; i < 8 * W; ++i)
+      if (!(fabsf(v[i]) < INFINITY)) code[i >> 2] = (code[i >> 2] & ~(0xFFu << (8 * (i & 3)))) | 0x7Fu << (8 * (i & 3));
   }
 }
 template <int W>
@@ -145,8 +156,6 @@ __global__ void __launch_bounds__(kAppendThreads, W == 2 ? 8 : 10) append_kernel
   const int64_t src0 = static_cast<int64_t>(bg) * p.T + (first - L);
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS, c0 = 8 * W * l;
   const bool on = c0 < p.d;
-  // the lanes of this row's group: the groups of a warp may leave the loop at different rows
-  const uint32_t group_mask = (GS == 32 ? 0xffffffffu : ((1u << (GS & 31)) - 1u)) << (threadIdx.x % 32 / GS * GS);
   constexpr int kGroups = kAppendThreads / GS;
   const __nv_bfloat16* src[2] = {static_cast<const __nv_bfloat16*>(p.k_new) + src0 * p.d + c0,
                                  static_cast<const __nv_bfloat16*>(p.v_new) + src0 * p.d + c0};
@@ -167,13 +176,14 @@ __global__ void __launch_bounds__(kAppendThreads, W == 2 ? 8 : 10) append_kernel
   }
   const int64_t page_row = (static_cast<int64_t>(page) * p.Hkv + g) * 64;
   uint8_t* dst[2] = {p.k_pool + (page_row + o0) * p.d + c0, p.v_pool + (page_row + o0) * p.d + c0};
-  for (int t = grp; t < rows; t += kGroups) {
+  for (int t0 = 0; t0 < rows; t0 += kGroups) {       // whole warps: rows past the last are zeros, and not stored
+    const int t = t0 + grp;
     load(nx, t + kGroups);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       uint32_t e, code[2 * W];
-      quantise_row<GS, W>(x[kv], group_mask, code, e);
-      if (!on) continue;
+      quantise_row<GS, W>(x[kv], code, e);
+      if (!on || t >= rows) continue;
       store_codes<W>(dst[kv] + t * p.d, code);
       if (l == 0) exps[kv][o0 + t] = static_cast<uint8_t>(e);
       if (kv == 0 && complete) store_codes<W>(codes + (o0 + t) * p.d + c0, code);
