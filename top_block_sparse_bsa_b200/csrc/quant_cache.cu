@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kAppendThreads, W == 2 ? 8 : 10) append_kernel
   griddep_wait();
   extern __shared__ uint4 smem_q[];
   uint8_t* codes = reinterpret_cast<uint8_t*>(smem_q);          // [64][d]
-  __shared__ uint8_t exps[2][64];
+  __shared__ __align__(4) uint8_t exps[2][64];
   const int j = blockIdx.x % p.touched;
   const int bg = blockIdx.x / p.touched;
   const int b = bg / p.Hkv, g = bg - b * p.Hkv;
@@ -205,19 +205,28 @@ __global__ void __launch_bounds__(kAppendThreads, W == 2 ? 8 : 10) append_kernel
     if (o >= o0 && o < o0 + rows) (kv ? p.v_exp : p.k_exp)[page_row + o] = exps[kv][o];
   }
   if (!complete) return;
-  // two channels a thread: a product is exact, so the fused form rounds each sum once, as the pooling does
-  for (int ch = 2 * threadIdx.x; ch < p.d; ch += 2 * kAppendThreads) {
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 16
-    for (int t = 0; t < 64; ++t) {
-      const __nv_fp8x2_storage_t two = *reinterpret_cast<const __nv_fp8x2_storage_t*>(codes + t * p.d + ch);
-      const float scale = two_to(exps[0][t]);
-      const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
-      s0 = fmaf(a.x, scale, s0);
-      s1 = fmaf(a.y, scale, s1);
+  // four channels a thread: a product is exact, so the fused form rounds each sum once, as the pooling does
+  for (int ch = 4 * threadIdx.x; ch < p.d; ch += 4 * kAppendThreads) {
+    uint64_t s01 = 0, s23 = 0;
+#pragma unroll 4
+    for (int t0 = 0; t0 < 64; t0 += 4) {
+      const uint32_t es = *reinterpret_cast<const uint32_t*>(&exps[0][t0]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t four = *reinterpret_cast<const uint32_t*>(codes + (t0 + i) * p.d + ch);
+        const float scale = __uint_as_float((i < 3 ? es << (23 - 8 * i) : es >> 1) & 0x7F800000u);
+        const uint64_t sc = f2_pack(scale, scale);
+        const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(four & 0xFFFFu, __NV_E4M3)));
+        const float2 c = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(four >> 16, __NV_E4M3)));
+        s01 = f2_fma(f2_pack(a.x, a.y), sc, s01);
+        s23 = f2_fma(f2_pack(c.x, c.y), sc, s23);
+      }
     }
-    *reinterpret_cast<float2*>(p.pooled + (static_cast<int64_t>(bg) * p.table_stride + blk) * p.d + ch) =
-        make_float2(__fdiv_rn(s0, 64.0f), __fdiv_rn(s1, 64.0f));
+    float4 v;
+    f2_unpack(s01, v.x, v.y);
+    f2_unpack(s23, v.z, v.w);
+    *reinterpret_cast<float4*>(p.pooled + (static_cast<int64_t>(bg) * p.table_stride + blk) * p.d + ch) =
+        make_float4(__fdiv_rn(v.x, 64.0f), __fdiv_rn(v.y, 64.0f), __fdiv_rn(v.z, 64.0f), __fdiv_rn(v.w, 64.0f));
   }
 }
 
