@@ -102,17 +102,31 @@ __device__ __forceinline__ void cp_async_wait_group() {
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// Ranges that `total` positions are cut into: none is empty.
-__device__ __forceinline__ int ranges(int64_t total, int most) {
-  return static_cast<int>(min(static_cast<int64_t>(most), total));
+// a / b, with the short division wherever 32 bits hold them: a 64-bit one takes about 0.3 us of a start-up or a switch
+// of rows.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
+// `total` positions cut into at most `most` ranges, none of them empty: range i is [i total / count,
+// (i+1) total / count), so borders of rows of equal length stay borders.
+struct Cut {
+  int64_t total, each;
+  int rest, count;
+  __device__ __forceinline__ Cut(int64_t all, int most) : total(all) {
+    count = static_cast<int>(min(static_cast<int64_t>(most), total));
+    each = count > 0 ? quotient(total, count) : 0;
+    rest = static_cast<int>(total - each * count);
+  }
+  __device__ __forceinline__ int64_t begin(int i) const {
+    return i * each + quotient(static_cast<int64_t>(i) * rest, count);
+  }
+  __device__ __forceinline__ int holds(int64_t x) const {      // the range of position x
+    return static_cast<int>(quotient((x + 1) * count + total - 1, total)) - 1;
+  }
+};
 __device__ __forceinline__ void team_sync(int team, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(threads) : "memory");
-}
-
-// The range c, [c total / C, (c+1) total / C), that holds x.
-__device__ __forceinline__ int range_of(int64_t x, int64_t total, int C) {
-  return static_cast<int>(((x + 1) * C + total - 1) / total) - 1;
 }
 
 // Without a list, pre[b] = blocks of the sequences before b, b <= B: a
@@ -177,7 +191,7 @@ __device__ __forceinline__ Item item_at(const QuantDecodeArgs& p, const int* pre
   int64_t row0;
   if (p.idx) {
     it.w = p.list_len;
-    const int bg = static_cast<int>(x / it.w);
+    const int bg = static_cast<int>(quotient(x, it.w));
     it.b = bg / p.Hkv;
     it.g = bg - it.b * p.Hkv;
     row0 = static_cast<int64_t>(bg) * it.w;
@@ -186,7 +200,7 @@ __device__ __forceinline__ Item item_at(const QuantDecodeArgs& p, const int* pre
     it.b = b;
     it.w = pre[b + 1] - pre[b];
     const int64_t seq0 = static_cast<int64_t>(pre[b]) * p.Hkv;
-    it.g = static_cast<int>((x - seq0) / it.w);
+    it.g = static_cast<int>(quotient(x - seq0, it.w));
     row0 = seq0 + static_cast<int64_t>(it.g) * it.w;
   }
   it.t0 = static_cast<int>(x - row0);
@@ -226,12 +240,11 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
   const int G = p.Hq / p.Hkv;
   const int64_t total = static_cast<int64_t>(p.idx ? p.B * p.list_len : pre[p.B]) * p.Hkv;
   // teams: the first of every block, then the second of every block, ...
-  const int team_warps = p.team_warps, team = warp / team_warps, tw = warp - team * team_warps;
+  const int team_warps = p.team_warps, team = warp >> (31 - __clz(team_warps)), tw = warp & (team_warps - 1);
   const int range = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-  const int C = ranges(total, p.num_ranges);
-  if (range >= C) return;
-  int64_t x = range * total / C;
-  const int64_t hi = (range + 1) * total / C;
+  const Cut cut(total, p.num_ranges);
+  if (range >= cut.count) return;
+  const int64_t x = cut.begin(range), hi = cut.begin(range + 1);
   int b_first = 0;
   if (p.idx == nullptr) {   // the sequence of position x: the last b with pre[b] * Hkv <= x
     int hi_b = p.B;
@@ -246,6 +259,7 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
   uint8_t* ring = smem_raw + warp * R * SB;
   const uint32_t ring_u32 = smem_u32(ring);
   Item li = item_at(p, pre, x, hi, b_first);   // item being loaded
+  Item it = li;                                 // item being worked on
   int l_no = 0;                                 // its number
   int l_base = tw - 32 * team_warps;            // first chunk of the batch held
   int l_len = 0;
@@ -314,34 +328,37 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
     cp_async_commit();
     if (lane == slot) meta = said;
   };
-  for (int s = 0; s < R; ++s) refill(s);
-
-  int head = 0;               // stage to be taken next
-  int b = b_first;
-  for (int no = 0; x < hi; ++no) {
-    const Item it = item_at(p, pre, x, hi, b);
-    b = it.b;
-    x = it.next;
-    // ---- the group's query heads, scaled by a power of two into fp16: a head's largest value goes to
-    // [2^10, 2^11), smaller ones keep their eight bits down to 2^-25 of it
-    uint32_t qf[NB][KS][2];
-    float qs[NB][2];        // logit factors of heads 2c, 2c+1 of each set
+  // the item's query heads as loaded, asked for before its keys or while the warps of the item before are joined
+  uint32_t qf[NB][KS][2];
+  auto load_q = [&](const Item& i) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int h = nb * 8 + r;
-      const __nv_bfloat16* qrow = p.q + (static_cast<int64_t>(b) * p.Hq + it.g * G + h) * D;
-      float amax = 0.0f;
+      const __nv_bfloat16* qrow = p.q + (static_cast<int64_t>(i.b) * p.Hq + i.g * G + h) * D;
 #pragma unroll
       for (int hf = 0; hf < KH; ++hf)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 v = h < G ? __ldg(reinterpret_cast<const uint4*>(qrow + hf * 64 + c * 16 + 8 * i))
+        for (int j = 0; j < 2; ++j) {
+          const uint4 v = h < G ? __ldg(reinterpret_cast<const uint4*>(qrow + hf * 64 + c * 16 + 8 * j))
                                 : make_uint4(0, 0, 0, 0);
-          qf[nb][hf * 4 + 2 * i][0] = v.x;
-          qf[nb][hf * 4 + 2 * i][1] = v.y;
-          qf[nb][hf * 4 + 2 * i + 1][0] = v.z;
-          qf[nb][hf * 4 + 2 * i + 1][1] = v.w;
+          qf[nb][hf * 4 + 2 * j][0] = v.x;
+          qf[nb][hf * 4 + 2 * j][1] = v.y;
+          qf[nb][hf * 4 + 2 * j + 1][0] = v.z;
+          qf[nb][hf * 4 + 2 * j + 1][1] = v.w;
         }
+    }
+  };
+  load_q(it);
+  for (int s = 0; s < R; ++s) refill(s);
+
+  int head = 0;               // stage to be taken next
+  for (int no = 0;; ++no) {
+    // ---- the group's query heads, scaled by a power of two into fp16: a head's largest value goes to
+    // [2^10, 2^11), smaller ones keep their eight bits down to 2^-25 of it
+    float qs[NB][2];        // logit factors of heads 2c, 2c+1 of each set
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float amax = 0.0f;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -502,6 +519,13 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
       head = head + 1 == R ? 0 : head + 1;
     }
 
+    const bool more = it.next < hi;
+    Item next = it;
+    if (more) {
+      next = item_at(p, pre, it.next, hi, it.b);
+      load_q(next);
+    }
+
     // ---- join the warps, then write the row or its partial record; a warp's O waits in its spare stage
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -533,24 +557,37 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
             mine[(2 * c + h) * (D / 2) + pair_at<D>(r, m, c)] = make_float2(O[nb][m][h], O[nb][m][2 + h]);
       }
       team_sync(team, 32 * team_warps);
-      const int heads = min(8, G - nb * 8), w0 = team * team_warps;
-      for (int e = threadIdx.x - 32 * w0; e < heads * (D / 2); e += 32 * team_warps) {
-        const int h = e / (D / 2), pr = e - h * (D / 2);         // query head of the set, channel pair
+      // a warp takes 32 channel pairs of a query head: lane k (of either half) holds warp k's share, the largest M
+      // and the sum of l come by exchange
+      const int units = min(8, G - nb * 8) * (D / 64), w0 = team * team_warps, mate = lane & 15;
+      for (int unit = tw; unit < units; unit += team_warps) {
+        const int h = unit / (D / 64), pr = unit % (D / 64) * 32 + lane;         // query head of the set, channel pair
         const int at = h * (D / 2) + pair_at<D>(pr / (D / 16), pr % (D / 16), h >> 1);
-        float mx = -INFINITY;
-        for (int k = w0; k < w0 + team_warps; ++k) mx = fmaxf(mx, sm_m[k][nb * 8 + h]);
-        float L = 0.0f, o0 = 0.0f, o1 = 0.0f;
-#pragma unroll 4
-        for (int k = w0; k < w0 + team_warps; ++k) {
-          const float mk = sm_m[k][nb * 8 + h];
-          if (mk == -INFINITY) continue;      // a warp without a key: it may have no spare stage
-          const float root = fast_exp2(0.5f * (mk - mx)), f = root * root;
-          const float2 v = reinterpret_cast<const float2*>(smem_raw + (k * R + sm_slot[k]) * SB)[at];
-          L += root * sm_l[k][nb * 8 + h] * root;
-          o0 += f * v.x;
-          o1 += f * v.y;
+        const float m_k = mate < team_warps ? sm_m[w0 + mate][nb * 8 + h] : -INFINITY;
+        float mx = m_k;
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float f = 0.0f, L = 0.0f;
+        int from = 0;
+        if (m_k != -INFINITY) {      // else a warp without a key: it may have no spare stage
+          const float root = fast_exp2(0.5f * (m_k - mx));
+          f = root * root;
+          L = root * sm_l[w0 + mate][nb * 8 + h] * root;
+          from = ((w0 + mate) * R + sm_slot[w0 + mate]) * SB;
         }
-        const int64_t orow = static_cast<int64_t>(b) * p.Hq + it.g * G + nb * 8 + h;
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        float o0 = 0.0f, o1 = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < team_warps; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, k);
+          const int from_k = __shfl_sync(0xffffffffu, from, k);
+          float2 v = make_float2(0.0f, 0.0f);
+          if (fk != 0.0f) v = reinterpret_cast<const float2*>(smem_raw + from_k)[at];
+          o0 += fk * v.x;
+          o1 += fk * v.y;
+        }
+        const int64_t orow = static_cast<int64_t>(it.b) * p.Hq + it.g * G + nb * 8 + h;
         if (whole) {
           const float inv = (mx == -INFINITY) ? 0.0f : static_cast<float>(1 << kDeep) / L;
           reinterpret_cast<uint32_t*>(p.o + orow * D)[pr] = pack_bf16x2(o0 * inv, o1 * inv);
@@ -567,8 +604,11 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
       }
       team_sync(team, 32 * team_warps);
     }
+    if (!more) break;
     if (spare >= 0) refill(spare);
+    it = next;
   }
+  cp_async_wait_group<0>();
 }
 
 // One block per (sequence, query head): rows cut by range borders are joined
@@ -593,9 +633,9 @@ __global__ void __launch_bounds__(D * PARTS) combine_kernel(const QuantDecodeArg
     if (p.lse && threadIdx.x == 0) p.lse[orow] = -INFINITY;
     return;
   }
-  const int C = ranges(total, p.num_ranges);
+  const Cut cut(total, p.num_ranges);
   const int64_t x0 = static_cast<int64_t>(before) * p.Hkv + static_cast<int64_t>(g) * w;
-  const int first = range_of(x0, total, C), n = range_of(x0 + w - 1, total, C) - first + 1;
+  const int first = cut.holds(x0), n = cut.holds(x0 + w - 1) - first + 1;
   if (n == 1) return;
   // the row begins inside range `first` (its record 1) and goes on in the next ones (their records 0)
   const float* rec = p.partial + (static_cast<int64_t>(first) * 2 * G + h) * (D + 4);
