@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
   Item it = li;                                 // item being worked on
   int l_no = 0;                                 // its number
   int l_base = tw - 32 * team_warps;            // first chunk of the batch held
+  int dealt = 0;                                // chunks of the items before: the next warp in turn takes the first
   int l_len = 0;
   unsigned l_left = 0u;                         // lanes whose chunk is still to be taken
   int my_row = 0, my_n = 0;                     // the lane's chunk: row of 16 in the pools, keys that count
@@ -278,10 +279,11 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
           l_base -= 32 * team_warps;
           break;
         }
+        dealt += 4 * (li.t1 - li.t0);
         li = item_at(p, pre, li.next, hi, li.b);
         l_len = seq_len(li.b);
         ++l_no;
-        l_base = tw;
+        l_base = (tw - dealt) & (team_warps - 1);
       }
       const int u = l_base + lane * team_warps;
       my_n = 0;
@@ -708,7 +710,9 @@ cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t st) {
 }  // namespace qdecode
 
 // One team of all warps an SM, or, while there are more rows than teams, two or
-// four smaller ones.  All multiprocessors take part: in short bursts 7/8 of them
+// four smaller ones; two also where rows of unknown lengths number more than half
+// of the SMs (128 rows of 1.5K to 3K tokens 22.1 us, in one team an SM 23.8; 96 of 2K
+// to 6K 25.5 and 26.2): such rows are cut, and one team loads while the other joins.  All multiprocessors take part: in short bursts 7/8 of them
 // draw more from memory than all (the whole cache of 16 sequences 371 us against
 // 397), but under steady load, where the power cap lowers the clock, they fall
 // behind (430 us against 405).
@@ -728,7 +732,7 @@ QuantSplit quant_decode_split(int num_sms, int group, int rows, bool list, int f
     s.ctas = forced;
     return s;
   }
-  for (int half = 0; half < 2 && rows > teams; ++half) {
+  for (int half = 0; half < 2 && (rows > teams || (half == 0 && !list && 2 * rows > teams)); ++half) {
     s.team_warps /= 2;
     teams *= 2;
   }
