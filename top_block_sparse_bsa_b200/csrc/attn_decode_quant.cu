@@ -14,8 +14,8 @@
 // for all its query heads, are the floor.  So the design keeps loads in
 // flight and spends few instructions a byte:
 //   - a warp takes 16 keys at a time through stages of its own: asynchronous
-//     copies bring 4 KB two to six chunks ahead and run on across the rows of
-//     its range; no barrier and no block-wide wait stands in the loop.
+//     copies bring 4 KB two chunks ahead and run on across the rows of its
+//     range; no barrier and no block-wide wait stands in the loop.
 //   - the codes become fp16 pairs by one conversion each (exact), and the
 //     products run on m16n8k16 matrix instructions with the keys (then the
 //     channels) as the 16 rows and eight query heads as the 8 columns.  The
@@ -40,9 +40,11 @@
 // cut by range borders leaves one partial record (M, l, O) per range, at most
 // two a team, and the second kernel joins them.
 //
-// 16 ragged sequences of 8 KV heads, 32 query heads: every block (2.5 GB) 382 to
-// 405 us (92 to 98% of the copy rate, by the clock under the power cap), 97 kept
-// blocks 39.6 us (79%); one sequence of 4001 tokens 10 us.
+// 16 ragged sequences of 8 KV heads, 32 query heads: every block (2.5 GB) 381 to
+// 389 us (96 to 98% of the copy rate, by the clock under the power cap), 97 kept
+// blocks 38.2 us (81%), of which some 4.5 pass before the first keys are there
+// (list, table, keys, one after the other, with cold code) and 1.3 in the join;
+// one sequence of 30000 tokens 18.9 us, of 4001 10.8.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -64,10 +66,11 @@ constexpr uint32_t kLeastExp = 56u;
 
 // NB = sets of eight query heads a warp carries; one block an SM: 16 warps of
 // two stages (three stages: 97 kept blocks x 16 sequences 41.6 us against 40.2),
-// or, where two sets (groups of 9 to 16 heads) take twice the registers, 8 warps
-// of six.
-__host__ __device__ constexpr int warps(int NB) { return NB == 1 ? 16 : 8; }
-__host__ __device__ constexpr int stages(int NB) { return NB == 1 ? 2 : 6; }
+// or, where two sets (groups of 9 to 16 heads) take more registers, 12 (128 query
+// heads, every block, us: 12 warps 482, 8 warps of six stages 507, 16 with the
+// queries in shared memory 486, slower in short calls; four stages 483).
+__host__ __device__ constexpr int warps(int NB) { return NB == 1 ? 16 : 12; }
+constexpr int kStages = 2;
 // a stage: 16 key rows, 16 value rows, their exponent bytes
 __host__ __device__ constexpr int stage_bytes(int D) { return 2 * 16 * D + 32; }
 
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
   constexpr int KS = D / 16;        // k-steps of q . K
   constexpr int MB = D / 16;        // 16-channel row blocks of O
   constexpr int VW = D / 32;        // 32-bit words of a V row per lane
-  constexpr int R = stages(NB);
+  constexpr int R = kStages;
   constexpr int SB = stage_bytes(D);
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ float sm_m[kWarps][8 * NB], sm_l[kWarps][8 * NB];
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
   const int G = p.Hq / p.Hkv;
   const int64_t total = static_cast<int64_t>(p.idx ? p.B * p.list_len : pre[p.B]) * p.Hkv;
   // teams: the first of every block, then the second of every block, ...
-  const int team_warps = p.team_warps, team = warp >> (31 - __clz(team_warps)), tw = warp & (team_warps - 1);
+  const int team_warps = p.team_warps, team = warp / team_warps, tw = warp - team * team_warps;
   const int range = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
   const Cut cut(total, p.num_ranges);
   if (range >= cut.count) return;
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
   Item it = li;                                 // item being worked on
   int l_no = 0;                                 // its number
   int l_base = tw - 32 * team_warps;            // first chunk of the batch held
-  int dealt = 0;                                // chunks of the items before: the next warp in turn takes the first
+  int turn = 0;                                 // the warp that takes the item's first chunk: dealt on across items
   int l_len = 0;
   unsigned l_left = 0u;                         // lanes whose chunk is still to be taken
   int my_row = 0, my_n = 0;                     // the lane's chunk: row of 16 in the pools, keys that count
@@ -279,11 +282,11 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
           l_base -= 32 * team_warps;
           break;
         }
-        dealt += 4 * (li.t1 - li.t0);
+        turn = (turn + 4 * (li.t1 - li.t0)) % team_warps;
         li = item_at(p, pre, li.next, hi, li.b);
         l_len = seq_len(li.b);
         ++l_no;
-        l_base = (tw - dealt) & (team_warps - 1);
+        l_base = tw - turn + (tw < turn ? team_warps : 0);
       }
       const int u = l_base + lane * team_warps;
       my_n = 0;
@@ -694,7 +697,7 @@ __global__ void __launch_bounds__(D * PARTS) combine_kernel(const QuantDecodeArg
 
 template <int D, int NB>
 cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(warps(NB)) * stages(NB) * stage_bytes(D) +
+  const size_t smem = static_cast<size_t>(warps(NB)) * kStages * stage_bytes(D) +
                       (a.idx ? 0 : (static_cast<size_t>(a.B) + 1) * sizeof(int));
   cudaError_t e = ensure_dynamic_smem<decode_kernel<D, NB>>(smem);
   if (e != cudaSuccess) return e;
@@ -712,10 +715,11 @@ cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t st) {
 // One team of all warps an SM, or, while there are more rows than teams, two or
 // four smaller ones; two also where rows of unknown lengths number more than half
 // of the SMs (128 rows of 1.5K to 3K tokens 22.1 us, in one team an SM 23.8; 96 of 2K
-// to 6K 25.5 and 26.2): such rows are cut, and one team loads while the other joins.  All multiprocessors take part: in short bursts 7/8 of them
-// draw more from memory than all (the whole cache of 16 sequences 371 us against
-// 397), but under steady load, where the power cap lowers the clock, they fall
-// behind (430 us against 405).
+// to 6K 25.5 and 26.2): such rows are cut, and one team loads while the other joins.
+// All multiprocessors take part: in short bursts 7/8 of them draw more from memory
+// than all (the whole cache of 16 sequences 371 us against 397), but under steady
+// load, where the power cap lowers the clock, they fall behind (430 us against
+// 405; both before the present join).
 // Ranges that end where rows end leave fewer records to join (97 kept blocks,
 // us: 128 rows on 128 ranges 42.3, on 148 45.0; 24 rows on 144 16.0, on 148
 // 19.0): from a list, where rows are equally long, as many ranges a row as fit
