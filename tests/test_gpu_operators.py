@@ -487,6 +487,17 @@ def test_decode_of_many_rows(bsa, B, Hkv, G):
     _check_decode(bsa, q, cache, lens, idx)
 
 
+@pytest.mark.parametrize("B,Hkv,G,d", [(12, 8, 4, 128), (11, 8, 12, 128), (9, 9, 16, 64), (18, 8, 9, 128), (3, 4, 16, 128),
+                                       (37, 2, 1, 64)])
+def test_decode_every_block_of_rows_cut_by_ranges(bsa, B, Hkv, G, d):
+    """Rows of lengths from none to 30 blocks, cut between teams of 3 to 16 warps; a range holds parts of several rows."""
+    r = np.random.default_rng(B * G)
+    lens = r.integers(0, 1900, B).tolist()
+    lens[1], lens[-1] = 0, 1920
+    q = torch.randn((B, Hkv * G, d), generator=torch.Generator().manual_seed(B)).bfloat16()
+    _check_decode(bsa, q, _cache(lens, Hkv, d, 30, seed=G), lens, None)
+
+
 @pytest.mark.parametrize("G", [2, 16])
 def test_decode_of_the_largest_batch(bsa, G):
     lens = [0] * 8192
