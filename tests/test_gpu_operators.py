@@ -498,6 +498,14 @@ def test_decode_every_block_of_rows_cut_by_ranges(bsa, B, Hkv, G, d):
     _check_decode(bsa, q, _cache(lens, Hkv, d, 30, seed=G), lens, None)
 
 
+@pytest.mark.parametrize("lens", [[0], [0, 0, 0], [0] * 200])
+def test_decode_of_empty_sequences_alone(bsa, lens):
+    q = torch.randn((len(lens), 8, 128), generator=torch.Generator().manual_seed(9)).bfloat16()
+    cache = _cache(lens, 2, 128, 3)
+    _check_decode(bsa, q, cache, lens, None)
+    _check_decode(bsa, q, cache, lens, np.zeros((len(lens), 2, 2), np.int32))
+
+
 @pytest.mark.parametrize("G", [2, 16])
 def test_decode_of_the_largest_batch(bsa, G):
     lens = [0] * 8192
