@@ -31,6 +31,47 @@ __device__ __forceinline__ __nv_bfloat162 as_pair(uint32_t v) { return *reinterp
 // A 16-bit code that orders as the bf16 values do, and back.
 __device__ __forceinline__ uint32_t code_value(uint32_t code) { return code & 0x8000u ? code & 0x7FFFu : ~code & 0xFFFFu; }
 
+// Sums over a row's warps, and what stands in the warps before; every warp calls them in step.  Two places in
+// turn: a warp may write the next sum while another still reads this one.
+template <int WARPS>
+struct Across {
+  int* place;       // [2][WARPS], shared
+  int turn = 0;
+  __device__ __forceinline__ explicit Across(int* shared) : place(shared) {}
+  __device__ __forceinline__ int sum(int v) {
+    int before;
+    return sum(v, before);
+  }
+  __device__ __forceinline__ int sum(int v, int& before) {
+    before = 0;
+    if constexpr (WARPS > 1) {
+      const int warp = threadIdx.x >> 5;
+      int* at = place + turn * WARPS;
+      turn ^= 1;
+      if ((threadIdx.x & 31) == 0) at[warp] = v;
+      __syncthreads();
+      v = 0;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        if (k < warp) before += at[k];
+        v += at[k];
+      }
+    }
+    return v;
+  }
+  __device__ __forceinline__ uint32_t max(uint32_t v) {
+    if constexpr (WARPS > 1) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(place) + turn * WARPS;
+      turn ^= 1;
+      if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = v;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) v = ::max(v, at[k]);
+    }
+    return v;
+  }
+};
+
 template <int PAIRS>
 __device__ __forceinline__ int count_ge(const uint32_t (&x)[PAIRS], uint32_t code) {
   const uint32_t t = code_value(code);
@@ -67,53 +108,54 @@ __device__ __forceinline__ uint32_t code_max(const uint32_t (&x)[PAIRS]) {
   return __reduce_max_sync(0xffffffffu, best);
 }
 
-// Pair p of lane l holds columns 64 p + 2 l and 64 p + 2 l + 1.
-template <int PAIRS>
-__global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ scores, int ncols,
+// Pair p of lane l of warp w holds columns 64 (PAIRS w + p) + 2 l and the next one.
+template <int PAIRS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) row_kernel(const float* __restrict__ scores, int ncols,
                                                  const int* __restrict__ lens, int rows_per_len, int block, int kb,
                                                  int* __restrict__ idx_out, int idx_stride,
                                                  int* __restrict__ count_out, uint32_t* __restrict__ status) {
   griddep_wait();   // the scores come from the kernel launched before
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col0 = warp * PAIRS * 64;                       // first column of this warp
   const int64_t r = blockIdx.x;
   const int len = lens[r / rows_per_len];
   const int n_all = len > 0 ? (len - 1) / block + 1 : 0;
-  if (n_all > ncols && lane == 0) atomicOr(status, BSA_DEV_BAD_INDEX);
+  if (n_all > ncols && threadIdx.x == 0) atomicOr(status, BSA_DEV_BAD_INDEX);
   const int n = min(n_all, ncols);
   const int ncand = max(n - 1, 0);
   const float* srow = scores + r * ncols;
   const float nan = __uint_as_float(0x7FFFFFFFu);
-  constexpr int kChunk = PAIRS < 32 ? PAIRS : 32;          // pairs of a lane's columns, per round
-  constexpr int kRounds = PAIRS / kChunk;
-  __shared__ float2 xs[PAIRS * 32 + PAIRS * 32 / kChunk];   // a gap behind each chunk keeps the lanes' banks apart
+  // a gap behind each lane's pairs keeps the lanes' banks apart
+  __shared__ float2 xs_all[WARPS][PAIRS * 32 + 32];
   __shared__ uint32_t member_key[32];
-  auto slot = [](int pair) { return pair + pair / kChunk; };
+  __shared__ int sums[2 * WARPS];
+  float2* xs = xs_all[warp];
+  Across<WARPS> across(sums);
+  auto slot = [](int pair) { return pair + pair / PAIRS; };
   uint32_t x[PAIRS];
-  // 32 pairs at a time, asked for together: no branch stands between the loads
+  // asked for together: no branch stands between the loads
   const bool even = ncols % 2 == 0 && (reinterpret_cast<uintptr_t>(scores) & 7u) == 0;
-  constexpr int kBatch = PAIRS < 32 ? PAIRS : 32;
-#pragma unroll
-  for (int p0 = 0; p0 < PAIRS; p0 += kBatch) {
-    float2 v[kBatch];
+  {
+    float2 v[PAIRS];
     if (even) {
 #pragma unroll
-      for (int p = 0; p < kBatch; ++p) {
-        const int j = 64 * (p0 + p) + 2 * lane;
+      for (int p = 0; p < PAIRS; ++p) {
+        const int j = col0 + 64 * p + 2 * lane;
         v[p] = j < ncand ? __ldg(reinterpret_cast<const float2*>(srow + j)) : make_float2(nan, nan);
       }
     } else {
 #pragma unroll
-      for (int p = 0; p < kBatch; ++p) {
-        const int j = 64 * (p0 + p) + 2 * lane;
+      for (int p = 0; p < PAIRS; ++p) {
+        const int j = col0 + 64 * p + 2 * lane;
         v[p].x = j < ncand ? __ldg(srow + j) : nan;
         v[p].y = j + 1 < ncand ? __ldg(srow + j + 1) : nan;
       }
     }
 #pragma unroll
-    for (int p = 0; p < kBatch; ++p) {
-      if (64 * (p0 + p) + 2 * lane + 1 >= ncand) v[p].y = nan;     // the row's next column, where it was read
-      x[p0 + p] = pack_bf16x2(v[p].x, v[p].y);
-      xs[slot(32 * (p0 + p) + lane)] = v[p];
+    for (int p = 0; p < PAIRS; ++p) {
+      if (col0 + 64 * p + 2 * lane + 1 >= ncand) v[p].y = nan;     // the row's next column, where it was read
+      x[p] = pack_bf16x2(v[p].x, v[p].y);
+      xs[slot(32 * p + lane)] = v[p];
     }
   }
   const int take = min(kb, ncand);
@@ -123,7 +165,7 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
   uint32_t t_code = 0xFFFFu, thresh = 0u;     // nothing is kept
   int ties = 0, remaining = 0, members = 0;
   if (take > 0) {
-    uint32_t lo = kNone, hi = max(code_max(x), kNone);
+    uint32_t lo = kNone, hi = max(across.max(code_max(x)), kNone);
     int at_least = ncand, above = 0;           // scores >= lo, > hi
     // the best scores lie in the octaves below the largest: 4 of them (128 codes each) are tried first, then 32
     uint32_t reach = 512u;
@@ -133,7 +175,7 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
         mid = hi > lo + reach ? hi - reach : mid;
         reach = reach == 512u ? 4096u : 0u;
       }
-      const int c = count_ge(x, mid);
+      const int c = across.sum(count_ge(x, mid));
       if (c >= take) {
         lo = mid;
         at_least = c;
@@ -148,60 +190,59 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
     members = at_least - above;
     if (lo == kNone) ties = remaining;        // every number, and NaNs (key 0) in index order
   }
-  // this lane's columns, round by round: bits of those that round above T, and to T
+  // this lane's columns, 2 PAIRS consecutive ones: bits of those that round above T, and to T
   __syncwarp();
   const __nv_bfloat162 t2 = as_pair(code_value(t_code) * 0x10001u);
-  uint64_t gt[kRounds], eq[kRounds];
-#pragma unroll
-  for (int rd = 0; rd < kRounds; ++rd) {
-    gt[rd] = eq[rd] = 0u;
-    const int pair0 = (rd * 32 + lane) * kChunk;       // of this lane
-    const int left = ncand - 2 * pair0;                // its candidates
-    if (left > 0 && take > 0) {
+  const int pair0 = lane * PAIRS, lane_col0 = col0 + 2 * pair0;
+  uint64_t gt = 0u, eq = 0u;
+  const int left = ncand - lane_col0;                // its candidates
+  if (left > 0 && take > 0) {
 #pragma unroll 8
-      for (int i = 0; i < kChunk; ++i) {
-        const float2 f = xs[slot(pair0 + i)];
-        const __nv_bfloat162 v = as_pair(pack_bf16x2(f.x, f.y));
-        uint32_t above_t, at_t;
-        if (t_code == kNone) {
-          above_t = __heq2_mask(v, v);
-          at_t = ~above_t;
-        } else {
-          above_t = __hgt2_mask(v, t2);
-          at_t = __heq2_mask(v, t2);
-        }
-        // a half of the mask is all ones or zeros: bits 0 and 31 tell
-        gt[rd] |= static_cast<uint64_t>((above_t & 1u) | (above_t >> 31 << 1)) << (2 * i);
-        eq[rd] |= static_cast<uint64_t>((at_t & 1u) | (at_t >> 31 << 1)) << (2 * i);
+    for (int i = 0; i < PAIRS; ++i) {
+      const float2 f = xs[slot(pair0 + i)];
+      const __nv_bfloat162 v = as_pair(pack_bf16x2(f.x, f.y));
+      uint32_t above_t, at_t;
+      if (t_code == kNone) {
+        above_t = __heq2_mask(v, v);
+        at_t = ~above_t;
+      } else {
+        above_t = __hgt2_mask(v, t2);
+        at_t = __heq2_mask(v, t2);
       }
-      if (left < 64) {
-        const uint64_t own = (1ull << left) - 1ull;
-        gt[rd] &= own;
-        eq[rd] &= own;
-      }
+      // a half of the mask is all ones or zeros: bits 0 and 31 tell
+      gt |= static_cast<uint64_t>((above_t & 1u) | (above_t >> 31 << 1)) << (2 * i);
+      eq |= static_cast<uint64_t>((at_t & 1u) | (at_t >> 31 << 1)) << (2 * i);
+    }
+    if (left < 64) {
+      const uint64_t own = (1ull << left) - 1ull;
+      gt &= own;
+      eq &= own;
     }
   }
-  auto key_at = [&](int rd, int bit) {
-    const float2 f = xs[slot((rd * 32 + lane) * kChunk + (bit >> 1))];
+  auto key_at = [&](int bit) {
+    const float2 f = xs[slot(pair0 + (bit >> 1))];
     return order_key(bit & 1 ? f.y : f.x);
+  };
+  // how many of the lanes and warps before, and of all
+  auto count_before = [&](int mine, int& before) {
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int warps_before;
+    const int all = across.sum(__shfl_sync(0xffffffffu, incl, 31), warps_before);
+    before = warps_before + incl - mine;
+    return all;
   };
   if (t_code != kNone && remaining < members) {
     if (members <= 32) {
       // the members' full keys in a list, each ranked against all
-      int mine_n = 0;
-#pragma unroll
-      for (int rd = 0; rd < kRounds; ++rd) mine_n += __popcll(eq[rd]);
-      int at = mine_n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += v;
-      }
-      at -= mine_n;
-#pragma unroll
-      for (int rd = 0; rd < kRounds; ++rd)
-        for (uint64_t m = eq[rd]; m; m &= m - 1) member_key[at++] = key_at(rd, __ffsll(m) - 1);
-      __syncwarp();
+      int at;
+      count_before(__popcll(eq), at);
+      for (uint64_t m = eq; m; m &= m - 1) member_key[at++] = key_at(__ffsll(m) - 1);
+      if constexpr (WARPS > 1) __syncthreads(); else __syncwarp();
       const uint32_t mine = lane < members ? member_key[lane] : 0u;
       int more = 0, same = 0;
       for (int i = 0; i < members; ++i) {
@@ -219,60 +260,36 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
       for (int bit = 31; bit >= 0; --bit) {
         const uint32_t cand = thresh | (1u << bit);
         int c = 0;
-#pragma unroll
-        for (int rd = 0; rd < kRounds; ++rd)
-          for (uint64_t m = eq[rd]; m; m &= m - 1) c += key_at(rd, __ffsll(m) - 1) >= cand ? 1 : 0;
-        if (__reduce_add_sync(0xffffffffu, c) >= remaining) thresh = cand;
+        for (uint64_t m = eq; m; m &= m - 1) c += key_at(__ffsll(m) - 1) >= cand ? 1 : 0;
+        if (across.sum(__reduce_add_sync(0xffffffffu, c)) >= remaining) thresh = cand;
       }
-#pragma unroll
-      for (int rd = 0; rd < kRounds; ++rd)
-        for (uint64_t m = eq[rd]; m; m &= m - 1) over += key_at(rd, __ffsll(m) - 1) > thresh ? 1 : 0;
-      ties = remaining - __reduce_add_sync(0xffffffffu, over);
+      for (uint64_t m = eq; m; m &= m - 1) over += key_at(__ffsll(m) - 1) > thresh ? 1 : 0;
+      ties = remaining - across.sum(__reduce_add_sync(0xffffffffu, over));
     }
+  }
+  uint64_t sel = gt, tie = 0u;
+  if (remaining > 0) {      // the same for the whole row
+    for (uint64_t m = eq; m; m &= m - 1) {
+      const uint32_t key = key_at(__ffsll(m) - 1);
+      const uint64_t bit = m & (0ull - m);
+      if (key > thresh) sel |= bit;
+      if (key == thresh) tie |= bit;
+    }
+    // ties in index order: the first of those not yet taken by columns before this lane's
+    int before;
+    count_before(__popcll(tie), before);
+    for (; tie != 0u && before < ties; tie &= tie - 1, ++before) sel |= tie & (0ull - tie);
   }
   int* out = idx_out + r * idx_stride;
-  int kept = 0, equal = 0;
-#pragma unroll
-  for (int rd = 0; rd < kRounds; ++rd) {
-    uint64_t sel = gt[rd], tie = 0u;
-    if (__any_sync(0xffffffffu, eq[rd] != 0u)) {
-      for (uint64_t m = eq[rd]; m; m &= m - 1) {
-        const uint32_t key = key_at(rd, __ffsll(m) - 1);
-        const uint64_t bit = m & (0ull - m);
-        if (key > thresh) sel |= bit;
-        if (key == thresh) tie |= bit;
-      }
-      // ties in index order: the first of those not yet taken by columns before this lane's
-      const int nt = __popcll(tie);
-      int before = nt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-      }
-      const int all = __shfl_sync(0xffffffffu, before, 31);
-      before += equal - nt;
-      for (; tie != 0u && before < ties; tie &= tie - 1, ++before) sel |= tie & (0ull - tie);
-      equal += all;
-    }
-    const int ns = __popcll(sel);
-    int at = ns;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, at, o);
-      if (lane >= o) at += v;
-    }
-    const int all = __shfl_sync(0xffffffffu, at, 31);
-    at += kept - ns;
-    for (; sel; sel &= sel - 1) out[at++] = (rd * 32 + lane) * 2 * kChunk + __ffsll(sel) - 1;
-    kept += all;
-  }
+  int at;
+  int kept = count_before(__popcll(sel), at);
+  for (; sel; sel &= sel - 1) out[at++] = lane_col0 + __ffsll(sel) - 1;
   if (n > 0) {
-    if (lane == 0) out[kept] = n - 1;
+    if (threadIdx.x == 0) out[kept] = n - 1;
     ++kept;
   }
-  for (int t = kept + lane; t < idx_stride; t += 32) out[t] = -1;
-  if (count_out && lane == 0) count_out[r] = kept;
+  for (int t = kept + threadIdx.x; t < idx_stride; t += 32 * WARPS) out[t] = -1;
+  if (count_out && threadIdx.x == 0) count_out[r] = kept;
 }
 
 }  // namespace topk_lens
@@ -280,8 +297,11 @@ __global__ void __launch_bounds__(32) row_kernel(const float* __restrict__ score
 cudaError_t launch_topk_lens(const float* scores, int rows, int ncols, const int* lens, int rows_per_len, int block,
                              int kb, int* idx_out, int idx_stride, int* count_out, uint32_t* status,
                              cudaStream_t st) {
-  auto kernel = ncols <= 64 * 8 ? topk_lens::row_kernel<8>
-                                : (ncols <= 64 * 32 ? topk_lens::row_kernel<32> : topk_lens::row_kernel<128>);
+  // a warp for up to 2048 columns, four for more
+  if (ncols > 64 * 32)
+    return launch_dependent(topk_lens::row_kernel<32, 4>, dim3(rows), dim3(128), 0, st, scores, ncols, lens, rows_per_len,
+                            block, kb, idx_out, idx_stride, count_out, status);
+  auto kernel = ncols <= 64 * 8 ? topk_lens::row_kernel<8, 1> : topk_lens::row_kernel<32, 1>;
   return launch_dependent(kernel, dim3(rows), dim3(32), 0, st, scores, ncols, lens, rows_per_len, block, kb, idx_out,
                           idx_stride, count_out, status);
 }
