@@ -657,7 +657,7 @@ def test_decode_pages_past_32_bits(bsa):
 
 # ------------------------------------------------------------------ selection
 
-@pytest.mark.parametrize("ncols", [1, 2, 31, 300, 512, 513, 2048, 2049, 8192])
+@pytest.mark.parametrize("ncols", [1, 2, 31, 300, 512, 513, 1024, 1025, 2048, 2049, 4097, 8192])
 def test_select_by_length(bsa, ncols):
     r = np.random.default_rng(ncols)
     per, block = 3, 64

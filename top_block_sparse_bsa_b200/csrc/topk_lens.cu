@@ -5,20 +5,21 @@
 // 核心模块 3; "稀疏注意力" tutorial §5), and columns from it on do not count: in a
 // growing cache they hold whatever was there before.
 //
-// One warp per row, the row's scores in its registers as bf16 pairs (rounded
-// to nearest, which keeps their order up to ties).  A row is a few KB, so
+// One warp per row (four past 2048 columns, whose counts meet in shared memory),
+// the row's scores in its registers as bf16 pairs (rounded to nearest, which
+// keeps their order up to ties).  A row is a few KB, so
 // instructions count, not bytes: the bf16 threshold T (the largest with at
 // least k scores >= T) is found by bisection of the 16-bit codes, 16 counts at
-// one compare and one add for two scores, without a barrier or shared memory.
+// one compare and one add for two scores.
 // Scores whose rounding is above T are kept; those that round to T (a few,
 // as a rule) are listed and ranked by their full keys, or, where more than 32
 // do, their lower key bits are bisected by 32 more counts over the row.
 // Equal scores: the lower index first.  NaN compares with nothing, so it ranks
 // last by itself.  The counts run over registers; then each lane takes 64
-// consecutive columns (16 in short rows) from shared memory, keeps what is
+// consecutive columns (32 or 16 in short rows) from shared memory, keeps what is
 // above T and what rounds to it as bits, and writes its kept columns behind
 // those of the lanes before it: no step waits for another column's.  2048 rows
-// of 1300 candidates: 11.7 us; a block of 256 threads a row with four 8-bit
+// of 1300 candidates: 11.5 us; a block of 256 threads a row with four 8-bit
 // histograms took 21.2, one 12-bit histogram and a ranked list 22.3, ballots
 // column by column instead of the lanes' bits 13.9.
 #include "kernels.h"
@@ -297,11 +298,14 @@ __global__ void __launch_bounds__(32 * WARPS) row_kernel(const float* __restrict
 cudaError_t launch_topk_lens(const float* scores, int rows, int ncols, const int* lens, int rows_per_len, int block,
                              int kb, int* idx_out, int idx_stride, int* count_out, uint32_t* status,
                              cudaStream_t st) {
-  // a warp for up to 2048 columns, four for more
+  // A warp for up to 2048 columns, four for more (us: 2048 rows of up to 8000 columns 33.0, by one warp 44.3; of 2048
+  // columns 11.6 by one warp, 13.0 by two, 15.8 by four); no wider than the row needs: a lane writes its columns one by
+  // one (2048 rows of up to 700 blocks 14.5 with 64 columns a lane, 9.5 with 32).
   if (ncols > 64 * 32)
     return launch_dependent(topk_lens::row_kernel<32, 4>, dim3(rows), dim3(128), 0, st, scores, ncols, lens, rows_per_len,
                             block, kb, idx_out, idx_stride, count_out, status);
-  auto kernel = ncols <= 64 * 8 ? topk_lens::row_kernel<8, 1> : topk_lens::row_kernel<32, 1>;
+  auto kernel = ncols <= 64 * 8 ? topk_lens::row_kernel<8, 1>
+                                : (ncols <= 64 * 16 ? topk_lens::row_kernel<16, 1> : topk_lens::row_kernel<32, 1>);
   return launch_dependent(kernel, dim3(rows), dim3(32), 0, st, scores, ncols, lens, rows_per_len, block, kb, idx_out,
                           idx_stride, count_out, status);
 }
