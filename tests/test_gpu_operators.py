@@ -391,7 +391,7 @@ def _cache(lens, Hkv, d, nb, seed=0, spread=1.0):
     return pools[0], pools[1], exps[0], exps[1], table
 
 
-def _check_decode(bsa, q, cache, lens, idx, scale=None, what="", far=0.0):
+def _check_decode(bsa, q, cache, lens, idx, scale=None, what="", far=0.0, least=0.0):
     B, Hq, d = q.shape
     k, v, ke, ve, table = cache
     Hkv, nb = k.shape[1], table.shape[1]
@@ -412,7 +412,7 @@ def _check_decode(bsa, q, cache, lens, idx, scale=None, what="", far=0.0):
     # unit adds); a weight moves by that, its fp16 rounding (2^-11) and the exponential (2^-22); the output is rounded
     # once more
     off = size * d * 2.0 ** -24 * 2 + 2.0 ** -20 + far
-    tol = HALF[torch.bfloat16] * np.abs(want) + (2.0 ** -11 + 2 * off)[..., None] * 1.01 * weight
+    tol = HALF[torch.bfloat16] * np.abs(want) + (2.0 ** -11 + 2 * off)[..., None] * 1.01 * weight + least
     err = np.abs(got - want)
     assert np.all(err <= tol), (what, np.unravel_index(np.argmax(err - tol), err.shape), (err - tol).max())
     none = np.isinf(want_lse)
@@ -545,6 +545,18 @@ def test_decode_with_rows_of_zero_values(bsa, zeros, e_rest):
     idx = np.full((3, 1, 4), -1, np.int32)
     idx[0, 0], idx[1, 0, :1], idx[2, 0, :3] = [0, 7, 38, 39], [0], [0, 5, 10]
     _check_decode(bsa, q, cache, lens, idx, scale=0.02, far=3 * 2.0 ** -18)
+
+
+@pytest.mark.parametrize("lo,hi", [(56, 60), (10, 20), (10, 90), (30, 246)])
+def test_decode_of_tiny_values(bsa, lo, hi):
+    # rows under exponent 56 (values under 2^-62) are off by at most 2^-94, absolute; their logits count in full
+    lens = [900, 17]
+    cache = _cache(lens, 2, 64, 15, seed=6)
+    r = np.random.default_rng(lo)
+    ve = np.where(cache[3] == 255, 255, r.integers(lo, hi + 1, cache[3].shape)).astype(np.uint8)
+    q = torch.randn((2, 8, 64), generator=torch.Generator().manual_seed(10)).bfloat16()
+    _check_decode(bsa, q, (*cache[:3], ve, cache[4]), lens, None, scale=0.02, far=3 * 2.0 ** -18,
+                  least=2.0 ** -94)
 
 
 def test_decode_ascending_logits_move_the_reference(bsa):
