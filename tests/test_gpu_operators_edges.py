@@ -1,0 +1,64 @@
+"""GPU tests at the edges of the norm + rotation, the quantised cache and the
+decode over it: rows that only pad a block's work, fields of a step that
+change between calls, magnitudes at the ends of the types, and equal bits on
+every run.
+
+Tolerances count roundings.  Half a step of a type is finfo(t).eps / 2
+relative to the value: bf16 2^-8, fp32 2^-24.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import plain_operators as plain
+from test_gpu_operators import HALF, _cache, _check_decode, _encode_step, _qkv, _rope_inputs, _weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bsa():
+    import top_block_sparse_bsa_b200 as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def pipe():
+    from top_block_sparse_bsa_b200 import pipeline
+    return pipeline
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean(bsa):
+    yield
+    code, flags = bsa.bsa_device_status(reset=True)
+    assert code == 0 and flags == 0, f"device status {code} flags {flags:#x}"
+
+
+# ------------------------------------------------------------ norm + rotation
+
+# N = 2500: enough tokens for full runs of heads (4 rows of bf16 or 2 of fp32 in flight), whose last one is partial
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [1, 21, 2500])
+@pytest.mark.parametrize("Hq,Hkv,d", [(1, 1, 64), (4, 2, 128), (5, 3, 64), (7, 1, 128), (8, 4, 64)])
+def test_weights_gradients_without_eps(pipe, Hq, Hkv, d, N, dtype):
+    """eps = 0: a head run's padding, whose mean of squares is 0, must not reach the weights' gradients."""
+    qkv = _qkv(1, N, Hq, Hkv, d, dtype, spread=0.5)
+    w = _weights(d, dtype, True)
+    freq, _ = _rope_inputs(d, "half")
+    g = torch.Generator().manual_seed(4)
+    grads = [torch.randn((1, h, N, d), generator=g) for h in (Hq, Hkv, Hkv)]
+    step = _encode_step(pipe, qkv.cuda(), Hq, Hkv, w, freq, "half", None, 1.0, eps=0.0)
+    got = step.backward(*(x.cuda() for x in grads))
+    want, (size, dw_size) = plain.encode_grad(qkv.double(), Hq, Hkv, w[0].double(), w[1].double(), 0.0, freq, "half",
+                                              None, 1.0, *(x.double() for x in grads))
+    err = (got["d_qkv"].cpu().double() - want[0]).abs()
+    # as with eps: two sums of d products, about 30 roundings on the longest way
+    assert bool((err <= HALF[dtype] * want[0].abs() + 2.0 ** -18 * size).all()), (err / (size + 1e-30)).max()
+    rows = N * max(Hq, Hkv)
+    for name, x, s in zip(("d_q_weight", "d_k_weight"), want[1:], dw_size):
+        # at most `rows` terms on one lane's way, each 2^-20 off, then 32 groups
+        err = (got[name].cpu().double() - x).abs()
+        assert bool((err <= ((rows + 32) * 2.0 ** -24 + 2.0 ** -20) * s).all()), name

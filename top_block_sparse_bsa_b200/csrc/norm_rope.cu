@@ -66,6 +66,9 @@ template <>
 struct Raw<float, 4> {
   float4 v;
   __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void fill(uint32_t bits) {
+    v.x = v.y = v.z = v.w = __uint_as_float(bits);
+  }
   __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
   __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
   __device__ __forceinline__ void pairs(uint64_t* x) const {
@@ -80,6 +83,7 @@ template <>
 struct Raw<__nv_bfloat16, 4> {
   uint2 v;
   __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void fill(uint32_t bits) { v = make_uint2(bits, bits); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = v; }
   __device__ __forceinline__ void pairs(uint64_t* x) const {
@@ -364,6 +368,9 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
   const int l = threadIdx.x % GS, grp = threadIdx.x / GS;
   const Lane m = lane_channels<LAYOUT, 4>(l, p.d, p.rot);
   const bool norm = p.q_weight != nullptr;
+  // rows past the last head: ones, with gradients of zero.  Zeros would have an infinite 1/rms where eps is 0, and
+  // 0 times that is a NaN in the weights' sums.
+  const uint32_t pad = !m.on ? 0u : (sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u);
   if (LAYOUT != LAYOUT_NONE) block_freqs(p.inv_freq, p.rot / 2, freqs);
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -409,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const Norm
         Raw<T, 4> xa[kRows], xb[kRows];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          ga[u].zero(), gb[u].zero(), xa[u].zero(), xb[u].zero();
+          ga[u].zero(), gb[u].zero(), xa[u].fill(pad), xb[u].fill(pad);
           if (m.on && live && h0 + u < to) {
             const float* src = dz + (h0 + u) * head_step;
             ga[u].load(src + m.a);
