@@ -62,3 +62,21 @@ def test_weights_gradients_without_eps(pipe, Hq, Hkv, d, N, dtype):
         # at most `rows` terms on one lane's way, each 2^-20 off, then 32 groups
         err = (got[name].cpu().double() - x).abs()
         assert bool((err <= ((rows + 32) * 2.0 ** -24 + 2.0 ** -20) * s).all()), name
+
+
+# --------------------------------------------------------------------- decode
+
+@pytest.mark.parametrize("Hq,d", [(4, 128), (16, 64)])
+@pytest.mark.parametrize("exponent,up", [(236, -117), (244, -124), (10, 100), (10, 115), (120, -100)])
+def test_decode_of_keys_and_queries_at_opposite_ends(bsa, exponent, up, Hq, d):
+    """Keys and queries near the two ends of fp32 with logits of ordinary size: no partial product leaves fp32."""
+    lens = [500, 33]
+    cache = _cache(lens, 1, d, 9, seed=3)
+    ke = np.where(cache[2] == 255, 255, np.clip(cache[2].astype(int) - 117 + exponent, 10, 246)).astype(np.uint8)
+    q = (2.0 ** up * torch.randn((2, Hq, d), generator=torch.Generator().manual_seed(6))).bfloat16()
+    # Some logits lie 100 apart here.  A weight is rounded to fp16 with the largest y = logit + value exponent of its
+    # warp's keys at 2^8 or above (the reference is a y, and no y passes it by more than 7 octaves at 2^15): an error of
+    # at most half of fp16's least step, 2^-25, is 2^-33 of the largest weight, times a code of at most 448, for each of
+    # at most 500 keys; the largest weight itself is at most 1 in units of the largest value exponent's power of two.
+    least = 500 * 2.0 ** -33 * 448 * 2.0 ** (int(cache[3][cache[3] != 255].max()) - 127)
+    _check_decode(bsa, q, (cache[0], cache[1], ke, cache[3], cache[4]), lens, None, least=least)

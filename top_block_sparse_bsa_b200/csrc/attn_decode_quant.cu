@@ -442,7 +442,9 @@ __global__ void __launch_bounds__(32 * warps(NB), 1) decode_kernel(const QuantDe
         bool high = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          yy[i] = f2_mul(f2_mul(f2_pack(S[nb][2 * i], S[nb][2 * i + 1]), f2_pack(kf[i], kf[i])), f2_pack(qs[nb][0], qs[nb][1]));
+          // the factors first: S 2^a alone may leave fp32 where the logit does not (large keys, small queries); their
+          // product leaves it only for logits past 2^95 or under 2^-99 (2^-33 <= |S| < 2^27)
+          yy[i] = f2_mul(f2_pack(S[nb][2 * i], S[nb][2 * i + 1]), f2_mul(f2_pack(kf[i], kf[i]), f2_pack(qs[nb][0], qs[nb][1])));
           if (n < 16 && r + 8 * i >= n) yy[i] = f2_pack(-INFINITY, -INFINITY);
           float y0, y1;
           f2_unpack(f2_add(yy[i], f2_pack(vb[i], vb[i])), y0, y1);
