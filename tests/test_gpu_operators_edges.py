@@ -13,7 +13,7 @@ import pytest
 import torch
 
 import plain_operators as plain
-from test_gpu_operators import HALF, _cache, _check_decode, _encode_step, _qkv, _rope_inputs, _weights
+from test_gpu_operators import HALF, _cache, _check_decode, _cuda, _encode_step, _qkv, _rope_inputs, _weights
 
 pytestmark = pytest.mark.gpu
 
@@ -62,6 +62,74 @@ def test_weights_gradients_without_eps(pipe, Hq, Hkv, d, N, dtype):
         # at most `rows` terms on one lane's way, each 2^-20 off, then 32 groups
         err = (got[name].cpu().double() - x).abs()
         assert bool((err <= ((rows + 32) * 2.0 ** -24 + 2.0 ** -20) * s).all()), name
+
+
+@pytest.mark.parametrize("change", ["inv_freq", "a shorter inv_freq", "layout", "rope_scale", "no rotation", "all"])
+def test_replaced_rotation_counts_from_the_next_call_on(pipe, change):
+    """A step whose frequencies, layout or scale are replaced gives, forward and backward, what a new step gives."""
+    Hq, Hkv, N, d = 4, 2, 40, 128
+    qkv = _qkv(1, N, Hq, Hkv, d, torch.bfloat16, spread=0.5).cuda()
+    w = _weights(d, torch.bfloat16, True)
+    freq, _ = _rope_inputs(d, "half")
+    g = torch.Generator().manual_seed(4)
+    grads = [torch.randn((1, h, N, d), generator=g).cuda() for h in (Hq, Hkv, Hkv)]
+    new = {"inv_freq": dict(inv_freq=freq / 4), "a shorter inv_freq": dict(inv_freq=freq[:24].clone()),
+           "layout": dict(layout=2), "rope_scale": dict(rope_scale=0.5), "no rotation": dict(inv_freq=None),
+           "all": dict(inv_freq=freq[:32] / 3, layout=2, rope_scale=1.5)}[change]
+    step = _encode_step(pipe, qkv, Hq, Hkv, w, freq, "half", None, 1.0)
+    first = step.run()["q"].clone()
+    step.backward(*grads)
+    for name, value in new.items():
+        setattr(step, name, _cuda(value) if name == "inv_freq" else value)
+    names = ("q", "k", "v", "d_qkv", "d_q_weight", "d_k_weight")
+    got = {**step.run(), **step.backward(*grads)}
+    f, layout, scale = new.get("inv_freq", freq), new.get("layout", 1), new.get("rope_scale", 1.0)
+    fresh = _encode_step(pipe, qkv, Hq, Hkv, w, f, ("none", "half", "pairs")[layout], None, scale)
+    want = {**fresh.run(), **fresh.backward(*grads)}
+    assert all(torch.equal(got[n], want[n]) for n in names)
+    assert not torch.equal(got["q"], first)
+    # and back, to a step that was built without a rotation too
+    step.inv_freq, step.layout, step.rope_scale = freq.cuda(), 1, 1.0
+    assert torch.equal(step.run()["q"], first)
+    bare = _encode_step(pipe, qkv, Hq, Hkv, w, None, "half", None, 1.0)
+    bare.run()
+    bare.inv_freq = freq.cuda()
+    assert torch.equal(bare.run()["q"], first)
+
+
+def test_frequencies_are_checked_like_every_tensor(bsa, pipe):
+    qkv = _qkv(1, 5, 2, 1, 64, torch.bfloat16).cuda()
+    freq, _ = _rope_inputs(64, "half")
+    step = _encode_step(pipe, qkv, 2, 1, (None, None), freq, "half", None, 1.0)
+    for bad in (freq, freq.float().cuda(), torch.stack([freq, freq], 1)[:, 0].cuda()[::2]):
+        step.inv_freq = bad
+        with pytest.raises(ValueError):
+            step.run()
+        with pytest.raises(ValueError):
+            step.backward(*(torch.zeros((1, h, 5, 64), device="cuda") for h in (2, 1, 1)))
+
+    class Elsewhere:                     # a tensor of another device
+        dtype, device, is_cuda = torch.float64, "cuda:99", True
+
+        def get_device(self):
+            return 99
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 256
+    rope = bsa.make_rope(bsa.BSA_ROPE_HALF, freq.cuda())
+    rope.freq = Elsewhere()
+    b = step.bufs
+    with pytest.raises(ValueError):
+        bsa.bsa_qkv_norm_rope(step.shape, qkv, None, None, 0.0, rope, None, b["q"], b["k"], b["v"])
+    # the frequencies live as long as the rotation made of them
+    rope = bsa.make_rope(bsa.BSA_ROPE_HALF, (freq / 2).cuda())
+    torch.full((32,), 7.0, dtype=torch.float64, device="cuda")
+    bsa.bsa_qkv_norm_rope(step.shape, qkv, None, None, 0.0, rope, None, b["q"], b["k"], b["v"])
+    want = _encode_step(pipe, qkv, 2, 1, (None, None), freq / 2, "half", None, 1.0).run()
+    assert torch.equal(b["q"], want["q"])
 
 
 # --------------------------------------------------------------------- decode

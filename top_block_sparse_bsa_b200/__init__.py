@@ -77,6 +77,7 @@ class BsaShape(ctypes.Structure):
 class BsaRope(ctypes.Structure):
     _fields_ = [("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
                 ("scale", ctypes.c_float)]
+    freq = None      # the tensor behind inv_freq, where make_rope made this
 
 
 _p = ctypes.c_void_p
@@ -353,8 +354,8 @@ def bsa_sparse_attn_decode_noalloc(shape: BsaShape, q, k_cache, v_cache, idx, id
 
 
 def make_rope(layout: int, inv_freq=None, scale: float = 1.0) -> Optional[BsaRope]:
-    """Rotation of the first 2*len(inv_freq) channels (inv_freq: float64 on the device, kept alive by the caller);
-    None for BSA_ROPE_NONE."""
+    """Rotation of the first 2*len(inv_freq) channels (inv_freq: float64 on the device, held by the result); None for
+    BSA_ROPE_NONE."""
     if layout == BSA_ROPE_NONE:
         if inv_freq is not None:
             raise ValueError("BSA_ROPE_NONE takes no frequencies")
@@ -363,7 +364,9 @@ def make_rope(layout: int, inv_freq=None, scale: float = 1.0) -> Optional[BsaRop
         raise ValueError("a rotation needs its frequencies")
     if inv_freq.dtype != torch.float64:
         raise ValueError(f"inv_freq is float64, got {inv_freq.dtype}")
-    return BsaRope(int(layout), 2 * inv_freq.numel(), _ptr(inv_freq), float(scale))
+    rope = BsaRope(int(layout), 2 * inv_freq.numel(), _ptr(inv_freq), float(scale))
+    rope.freq = inv_freq
+    return rope
 
 
 def bsa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: int = BSA_ROPE_PLAIN, factor: float = 1.0,
@@ -409,17 +412,30 @@ def _here(stream):
 
 def _token_rows(what: str, x, shape: BsaShape, dtype, device: int):
     """Pointer and token stride of x [B, Nq, Hq+2Hkv, d]: dense but for the distance between tokens."""
-    heads, d = shape.Hq + 2 * shape.Hkv, shape.d
-    size, stride = x.size(), x.stride()
     if x.dtype is not dtype or x.get_device() != device:
         _refuse(what, x, dtype, device)
+    size, heads, d = x.size(), shape.Hq + 2 * shape.Hkv, shape.d
     if size != (shape.B, shape.Nq, heads, d):
         raise ValueError(f"{what} is [{shape.B}, {shape.Nq}, {heads}, {d}], got {list(size)}")
+    if x.is_contiguous():
+        return x.data_ptr(), heads * d
+    stride = x.stride()
     token = stride[1] if shape.Nq > 1 else (stride[0] if shape.B > 1 else heads * d)
     if (d > 1 and stride[3] != 1) or (heads > 1 and stride[2] != d) or \
             (shape.B > 1 and stride[0] != shape.Nq * token):
         raise ValueError(f"{what}: heads and channels are dense, tokens evenly apart")
     return x.data_ptr(), token
+
+
+def _rope_at(rope: Optional[BsaRope], device: int):
+    """The library's argument for a rotation, its frequencies checked as every tensor is."""
+    if rope is None:
+        return None
+    freq = rope.freq
+    if freq is not None:
+        if freq.get_device() != device or freq.data_ptr() != rope.inv_freq:
+            rope.inv_freq = _at("inv_freq", freq, torch.float64, device)
+    return ctypes.byref(rope)
 
 
 def _size(t) -> int:
@@ -438,7 +454,7 @@ def bsa_qkv_norm_rope(shape: BsaShape, qkv, q_weight, k_weight, eps: float, rope
     src, token_stride = _token_rows("qkv", qkv, shape, t, dev)
     code = lib.bsa_qkv_norm_rope(
         ctypes.byref(shape), src, token_stride, _at("q_weight", q_weight, t, dev), _at("k_weight", k_weight, t, dev),
-        eps, ctypes.byref(rope) if rope is not None else None, _at("positions", positions, torch.int32, dev),
+        eps, _rope_at(rope, dev), _at("positions", positions, torch.int32, dev),
         _at("q", q, t, dev), _at("k", k, t, dev), _at("v", v, t, dev), st)
     if code:
         raise BsaError("bsa_qkv_norm_rope", code)
@@ -453,7 +469,7 @@ def bsa_qkv_norm_rope_bwd(shape: BsaShape, qkv, q_weight, k_weight, eps: float, 
     dst, d_token_stride = _token_rows("d_qkv", d_qkv, shape, t, dev)
     code = lib.bsa_qkv_norm_rope_bwd(
         ctypes.byref(shape), src, token_stride, _at("q_weight", q_weight, t, dev), _at("k_weight", k_weight, t, dev),
-        eps, ctypes.byref(rope) if rope is not None else None, _at("positions", positions, torch.int32, dev),
+        eps, _rope_at(rope, dev), _at("positions", positions, torch.int32, dev),
         _at("dq", dq, f32, dev), _at("dk", dk, f32, dev), _at("dv", dv, f32, dev), dst, d_token_stride,
         _at("d_q_weight", d_q_weight, f32, dev), _at("d_k_weight", d_k_weight, f32, dev),
         _at("workspace", workspace, torch.uint8, dev), _size(workspace), st)

@@ -380,14 +380,28 @@ class HssaStep:
         return b
 
 
+class _Replaceable:
+    """A step whose fields may be replaced between calls: what is derived from them is derived again at the next one
+    (``_derive``)."""
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__["_current"] = False
+
+    def _bring_up(self):
+        self._derive()
+        self.__dict__["_current"] = True
+
+
 @dataclass
-class QkvStep:
+class QkvStep(_Replaceable):
     """From a fused projection qkv [B,N,Hq+2Hkv,d] to q [B,Hq,N,d], k and v [B,Hkv,N,d] for the steps here: RMS
     norm of every query and key head (q_weight and k_weight [d], or None), rotation by position, head-major order.
 
     inv_freq: float64 [rot_dim/2] on the device (bsa_rope_inv_freq; None: no rotation); positions [B,N] int32 or
-    None (0..N-1); rope_scale: the factor of a scaling for long contexts.  For decode (N = 1), q is
-    bufs["q"][:, :, 0] and k, v are PagedDecodeStep.append's or QuantDecodeStep.append's k_new, v_new."""
+    None (0..N-1); rope_scale: the factor of a scaling for long contexts.  A field replaced later counts from the next
+    call on.  For decode (N = 1), q is bufs["q"][:, :, 0] and k, v are PagedDecodeStep.append's or
+    QuantDecodeStep.append's k_new, v_new."""
     qkv: torch.Tensor
     Hq: int
     Hkv: int
@@ -410,13 +424,18 @@ class QkvStep:
             if w is not None and w.shape != (d,):
                 raise ValueError(f"a norm's weight is [{d}], got {list(w.shape)}")
         self.shape = make_shape(B, self.Hq, self.Hkv, N, N, d, 1, self.qkv.dtype)
-        self.rope = make_rope(self.layout if self.inv_freq is not None else BSA_ROPE_NONE, self.inv_freq,
-                              self.rope_scale)
+        self._bring_up()
         b = self.bufs
         for name, heads in (("q", self.Hq), ("k", self.Hkv), ("v", self.Hkv)):
             b.setdefault(name, torch.empty((B, heads, N, d), dtype=self.qkv.dtype, device=self.qkv.device))
 
+    def _derive(self):
+        self.rope = make_rope(self.layout if self.inv_freq is not None else BSA_ROPE_NONE, self.inv_freq,
+                              self.rope_scale)
+
     def run(self, stream=None):
+        if not self._current:
+            self._bring_up()
         b = self.bufs
         bsa_qkv_norm_rope(self.shape, self.qkv, self.q_weight, self.k_weight, self.eps, self.rope, self.positions,
                           b["q"], b["k"], b["v"], stream=stream)
@@ -425,6 +444,8 @@ class QkvStep:
     def backward(self, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, stream=None):
         """Gradients d_qkv (qkv's type, dense) and, with weights, d_q_weight and d_k_weight (fp32) from fp32 dq, dk,
         dv, as PrefillStep.backward gives them."""
+        if not self._current:
+            self._bring_up()
         B, N, H, d = self.qkv.shape
         for name, g, heads in (("dq", dq, self.Hq), ("dk", dk, self.Hkv), ("dv", dv, self.Hkv)):
             if g.shape != (B, heads, N, d):
