@@ -132,6 +132,27 @@ def test_frequencies_are_checked_like_every_tensor(bsa, pipe):
     assert torch.equal(b["q"], want["q"])
 
 
+def test_replaced_tensors_of_the_same_size_count_from_the_next_call_on(pipe):
+    Hq, Hkv, N, d = 4, 2, 40, 128
+    freq, _ = _rope_inputs(d, "half")
+    g = torch.Generator().manual_seed(4)
+    grads = [torch.randn((2, h, N, d), generator=g).cuda() for h in (Hq, Hkv, Hkv)]
+    pos = [torch.randint(0, 5000, (2, N), generator=g).int() for _ in range(2)]
+    qkv = [_qkv(2, N, Hq, Hkv, d, torch.bfloat16, seed=s, spread=0.5).cuda() for s in (0, 1)]
+    w = [_weights(d, torch.bfloat16, True, seed=s) for s in (5, 6)]
+    step = _encode_step(pipe, qkv[0], Hq, Hkv, w[0], freq, "half", pos[0], 1.0)
+    step.run()
+    step.backward(*grads)
+    step.qkv, step.positions, step.q_weight, step.k_weight = qkv[1], pos[1].cuda(), w[1][0].cuda(), w[1][1].cuda()
+    got = {**step.run(), **step.backward(*grads)}
+    fresh = _encode_step(pipe, qkv[1], Hq, Hkv, w[1], freq, "half", pos[1], 1.0)
+    want = {**fresh.run(), **fresh.backward(*grads)}
+    assert all(torch.equal(got[n], want[n]) for n in ("q", "k", "v", "d_qkv", "d_q_weight", "d_k_weight"))
+    step.q_weight = step.k_weight = None                     # without norms, gradients of no weights
+    fresh = _encode_step(pipe, qkv[1], Hq, Hkv, (None, None), freq, "half", pos[1], 1.0)
+    assert torch.equal(step.backward(*grads)["d_qkv"], fresh.backward(*grads)["d_qkv"])
+
+
 # --------------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("Hq,d", [(4, 128), (16, 64)])
@@ -148,3 +169,30 @@ def test_decode_of_keys_and_queries_at_opposite_ends(bsa, exponent, up, Hq, d):
     # at most 500 keys; the largest weight itself is at most 1 in units of the largest value exponent's power of two.
     least = 500 * 2.0 ** -33 * 448 * 2.0 ** (int(cache[3][cache[3] != 255].max()) - 127)
     _check_decode(bsa, q, (cache[0], cache[1], ke, cache[3], cache[4]), lens, None, least=least)
+
+
+def _decode_step(pipe, seed, lens, kb, **kw):
+    cache = _cache(lens, 2, 128, 12, seed=seed)
+    q = torch.randn((len(lens), 8, 128), generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+    step = pipe.QuantDecodeStep(q, *(torch.from_numpy(x).cuda() for x in cache),
+                                torch.tensor(lens, dtype=torch.int32).cuda(), kb=kb, **kw)
+    if kb is not None:
+        step.bufs["kbar"].copy_(torch.randn(step.bufs["kbar"].shape, generator=torch.Generator().manual_seed(seed)))
+    return step
+
+
+def test_replaced_decode_tensors_of_the_same_size_count_from_the_next_call_on(pipe):
+    a, b = _decode_step(pipe, 1, [700, 40, 333], 3), _decode_step(pipe, 2, [64, 768, 0], 2)
+    want = {n: b.run()[n].clone() for n in ("o", "lse", "count")}
+    a.run()
+    for name in ("q", "k_pool", "v_pool", "k_exp", "v_exp", "block_table", "seq_lens"):
+        setattr(a, name, getattr(b, name))
+    a.kb = 2                                                 # fewer than it was built for: the lists end earlier
+    a.bufs["kbar"].copy_(b.bufs["kbar"])
+    got = a.run()
+    assert torch.equal(got["idx"][..., :3], b.bufs["idx"]) and bool((got["idx"][..., 3:] == -1).all())
+    # the lists' lengths decide where rows are cut, and so in which order a row's keys are summed: an output may fall on
+    # the other side of a rounding
+    assert torch.equal(got["count"], want["count"])
+    assert torch.allclose(got["o"].float(), want["o"].float(), rtol=2.0 ** -7, atol=2.0 ** -9)
+    assert torch.allclose(got["lse"], want["lse"], rtol=2.0 ** -18)

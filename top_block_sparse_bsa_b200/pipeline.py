@@ -380,17 +380,30 @@ class HssaStep:
         return b
 
 
+def _fits(what: str, t: Optional[torch.Tensor], *shape: int):
+    if t is not None and t.shape != shape:
+        raise ValueError(f"{what} is {list(shape)}, got {list(t.shape)}")
+
+
+def _buffer(bufs: Dict[str, torch.Tensor], name: str, shape, dtype, device, zero: bool = False):
+    """Makes the buffer of that name, or checks that the caller's own is large enough."""
+    if name not in bufs:
+        bufs[name] = (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+    elif bufs[name].numel() < math.prod(shape):
+        raise ValueError(f"bufs[{name!r}] is {list(shape)}, got {list(bufs[name].shape)}")
+
+
 class _Replaceable:
-    """A step whose fields may be replaced between calls: what is derived from them is derived again at the next one
-    (``_derive``)."""
+    """A step whose fields may be replaced between calls: at the next one they are checked, against the sizes that the
+    step was built for, and what is derived from them is derived again (``_derive``)."""
 
     def __setattr__(self, name, value):
-        self.__dict__[name] = value
-        self.__dict__["_current"] = False
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_current", False)
 
     def _bring_up(self):
         self._derive()
-        self.__dict__["_current"] = True
+        object.__setattr__(self, "_current", True)
 
 
 @dataclass
@@ -399,8 +412,8 @@ class QkvStep(_Replaceable):
     norm of every query and key head (q_weight and k_weight [d], or None), rotation by position, head-major order.
 
     inv_freq: float64 [rot_dim/2] on the device (bsa_rope_inv_freq; None: no rotation); positions [B,N] int32 or
-    None (0..N-1); rope_scale: the factor of a scaling for long contexts.  A field replaced later counts from the next
-    call on.  For decode (N = 1), q is bufs["q"][:, :, 0] and k, v are PagedDecodeStep.append's or
+    None (0..N-1); rope_scale: the factor of a scaling for long contexts.  A field replaced by another of its size
+    counts from the next call on.  For decode (N = 1), q is bufs["q"][:, :, 0] and k, v are PagedDecodeStep.append's or
     QuantDecodeStep.append's k_new, v_new."""
     qkv: torch.Tensor
     Hq: int
@@ -418,20 +431,21 @@ class QkvStep(_Replaceable):
         B, N, H, d = self.qkv.shape
         if H != self.Hq + 2 * self.Hkv:
             raise ValueError(f"qkv has {H} heads a token, not {self.Hq} + 2 * {self.Hkv}")
-        if self.positions is not None and self.positions.shape != (B, N):
-            raise ValueError(f"positions are [{B}, {N}], got {list(self.positions.shape)}")
-        for w in (self.q_weight, self.k_weight):
-            if w is not None and w.shape != (d,):
-                raise ValueError(f"a norm's weight is [{d}], got {list(w.shape)}")
         self.shape = make_shape(B, self.Hq, self.Hkv, N, N, d, 1, self.qkv.dtype)
         self._bring_up()
-        b = self.bufs
-        for name, heads in (("q", self.Hq), ("k", self.Hkv), ("v", self.Hkv)):
-            b.setdefault(name, torch.empty((B, heads, N, d), dtype=self.qkv.dtype, device=self.qkv.device))
 
     def _derive(self):
+        s = self.shape
+        _fits("qkv", self.qkv, s.B, s.Nq, s.Hq + 2 * s.Hkv, s.d)
+        if (self.Hq, self.Hkv) != (s.Hq, s.Hkv):
+            raise ValueError(f"this step has {s.Hq} query and {s.Hkv} key heads")
+        _fits("positions", self.positions, s.B, s.Nq)
+        _fits("q_weight", self.q_weight, s.d)
+        _fits("k_weight", self.k_weight, s.d)
         self.rope = make_rope(self.layout if self.inv_freq is not None else BSA_ROPE_NONE, self.inv_freq,
                               self.rope_scale)
+        for name, heads in (("q", s.Hq), ("k", s.Hkv), ("v", s.Hkv)):
+            _buffer(self.bufs, name, (s.B, heads, s.Nq, s.d), self.qkv.dtype, self.qkv.device)
 
     def run(self, stream=None):
         if not self._current:
@@ -454,25 +468,27 @@ class QkvStep(_Replaceable):
         dev = self.qkv.device
         if "d_qkv" not in b:
             b["d_qkv"] = torch.empty((B, N, H, d), dtype=self.qkv.dtype, device=dev)
-        if self.q_weight is not None and "d_q_weight" not in b:
-            b["d_q_weight"] = torch.empty((d,), dtype=torch.float32, device=dev)
-            b["d_k_weight"] = torch.empty((d,), dtype=torch.float32, device=dev)
-            b["qkv_workspace"] = torch.empty((bsa_workspace_bytes_norm_rope(self.shape),), dtype=torch.uint8,
-                                             device=dev)
+        weights = (None, None, None)
+        if self.q_weight is not None:
+            if "qkv_workspace" not in b:
+                _buffer(b, "d_q_weight", (d,), torch.float32, dev)
+                _buffer(b, "d_k_weight", (d,), torch.float32, dev)
+                b["qkv_workspace"] = torch.empty((bsa_workspace_bytes_norm_rope(self.shape),), dtype=torch.uint8,
+                                                 device=dev)
+            weights = (b["d_q_weight"], b["d_k_weight"], b["qkv_workspace"])
         bsa_qkv_norm_rope_bwd(self.shape, self.qkv, self.q_weight, self.k_weight, self.eps, self.rope, self.positions,
-                              dq, dk, dv, b["d_qkv"], b.get("d_q_weight"), b.get("d_k_weight"),
-                              b.get("qkv_workspace"), stream=stream)
+                              dq, dk, dv, b["d_qkv"], *weights, stream=stream)
         return b
 
 
 @dataclass
-class QuantDecodeStep:
+class QuantDecodeStep(_Replaceable):
     """Decode over a paged KV cache of 8 bits whose sequences have their own lengths: pools [P,Hkv,64,d] of e4m3
     codes, exponents [P,Hkv,64], a block table [B, nb] and seq_lens [B] (int32, the tokens each sequence holds;
     the caller advances them after ``append``).  ``append`` quantises new tokens and pools completed blocks;
     ``select`` scores the query against the pooled summary and keeps each sequence's kb best history blocks and
     its last; ``attend`` gathers them through the table.  kb None: every block is attended, nothing is selected.
-    ``read`` gives tokens back as dense rows."""
+    ``read`` gives tokens back as dense rows.  A field may be replaced by another of its size."""
     q: torch.Tensor
     k_pool: torch.Tensor
     v_pool: torch.Tensor
@@ -496,19 +512,28 @@ class QuantDecodeStep:
         self.idx_stride = 0 if self.kb is None else self.kb + 1
         if self.softmax_scale is None:
             self.softmax_scale = 1.0 / math.sqrt(d)
-        dev = _dev(self.q)
-        f32 = torch.float32
-        b = self.bufs
-        if self.kb is not None:
-            b.setdefault("kbar", torch.zeros((B, Hkv, nb, d), dtype=f32, device=dev))
-            b.setdefault("qbar", torch.empty((B, Hkv, d), dtype=f32, device=dev))
-            b.setdefault("scores", torch.empty((B, Hkv, nb), dtype=f32, device=dev))
-            b.setdefault("idx", torch.empty((B, Hkv, self.idx_stride), dtype=torch.int32, device=dev))
-            b.setdefault("count", torch.empty((B, Hkv), dtype=torch.int32, device=dev))
-        ws = bsa_workspace_bytes(BSA_OP_DECODE_QUANT, self.shape, self.idx_stride)
-        b.setdefault("workspace", torch.empty((max(ws, 256),), dtype=torch.uint8, device=dev))
-        b.setdefault("o", torch.empty_like(self.q))
-        b.setdefault("lse", torch.empty((B, Hq), dtype=f32, device=dev))
+        self._bring_up()
+
+    def _derive(self):
+        s, b, dev, f32 = self.shape, self.bufs, _dev(self.q), torch.float32
+        _fits("q", self.q, s.B, s.Hq, s.d)
+        _fits("k_pool", self.k_pool, self.k_pool.shape[0], s.Hkv, self.block, s.d)
+        _fits("block_table", self.block_table, s.B, self.nb)
+        _fits("seq_lens", self.seq_lens, s.B)
+        if (self.kb is None) != (self.idx_stride == 0) or (self.kb is not None and self.kb >= self.idx_stride):
+            raise ValueError(f"this step was built for kb {f'< {self.idx_stride}' if self.idx_stride else 'None'}, "
+                             f"got {self.kb}")
+        if self.idx_stride:
+            _buffer(b, "kbar", (s.B, s.Hkv, self.nb, s.d), f32, dev, zero=True)
+            _buffer(b, "qbar", (s.B, s.Hkv, s.d), f32, dev)
+            _buffer(b, "scores", (s.B, s.Hkv, self.nb), f32, dev)
+            _buffer(b, "idx", (s.B, s.Hkv, self.idx_stride), torch.int32, dev)
+            _buffer(b, "count", (s.B, s.Hkv), torch.int32, dev)
+        if "workspace" not in b:
+            ws = bsa_workspace_bytes(BSA_OP_DECODE_QUANT, s, self.idx_stride)
+            b["workspace"] = torch.empty((max(ws, 256),), dtype=torch.uint8, device=dev)
+        _buffer(b, "o", (s.B, s.Hq, s.d), self.q.dtype, dev)
+        _buffer(b, "lse", (s.B, s.Hq), f32, dev)
 
     def _rows_shape(self, T: int, dtype):
         s = self.shape
@@ -516,6 +541,8 @@ class QuantDecodeStep:
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, new_lens: Optional[torch.Tensor] = None, stream=None):
         """Quantise k_new/v_new [B,Hkv,T,d] (t < new_lens[b]) behind seq_lens[b] tokens; completed blocks are pooled."""
+        if not self._current:
+            self._bring_up()
         s = self.shape
         if k_new.shape != v_new.shape or k_new.shape[:2] != (s.B, s.Hkv) or k_new.shape[3] != s.d:
             raise ValueError(f"new keys and values are [{s.B}, {s.Hkv}, T, {s.d}], got {list(k_new.shape)}")
@@ -527,6 +554,8 @@ class QuantDecodeStep:
 
     def read(self, k_out: torch.Tensor, v_out: torch.Tensor, starts: Optional[torch.Tensor] = None, stream=None):
         """Tokens starts[b] + t into row t of k_out/v_out [B,Hkv,T,d] (bf16 or fp32), as far as the sequence goes."""
+        if not self._current:
+            self._bring_up()
         s = self.shape
         if k_out.shape != v_out.shape or k_out.shape[:2] != (s.B, s.Hkv) or k_out.shape[3] != s.d:
             raise ValueError(f"rows read back are [{s.B}, {s.Hkv}, T, {s.d}], got {list(k_out.shape)}")
@@ -536,6 +565,8 @@ class QuantDecodeStep:
                              self.v_exp, self.block_table, self.seq_lens, k_out, v_out, starts=starts, stream=stream)
 
     def select(self, stream=None):
+        if not self._current:
+            self._bring_up()
         if self.kb is None:
             raise ValueError("this step attends every block (kb None): there is nothing to select")
         b, s = self.bufs, self.shape
@@ -544,6 +575,8 @@ class QuantDecodeStep:
                              self.idx_stride, b["count"], stream=stream)
 
     def attend(self, idx: Optional[torch.Tensor] = None, stream=None, with_lse: bool = True):
+        if not self._current:
+            self._bring_up()
         b = self.bufs
         if idx is None:
             idx = b.get("idx")
