@@ -196,3 +196,13 @@ def test_replaced_decode_tensors_of_the_same_size_count_from_the_next_call_on(pi
     assert torch.equal(got["count"], want["count"])
     assert torch.allclose(got["o"].float(), want["o"].float(), rtol=2.0 ** -7, atol=2.0 ** -9)
     assert torch.allclose(got["lse"], want["lse"], rtol=2.0 ** -18)
+
+
+def test_a_step_of_every_block_attends_every_block_with_another_step_s_buffers(pipe):
+    lens = [700, 40, 333]
+    kept = _decode_step(pipe, 1, lens, 3)
+    alone = _decode_step(pipe, 1, lens, None).run()["o"].clone()
+    workspace = torch.empty_like(_decode_step(pipe, 1, lens, None).bufs["workspace"])
+    every = _decode_step(pipe, 1, lens, None, bufs={**kept.bufs, "workspace": workspace})
+    few = kept.run()["o"].clone()
+    assert torch.equal(every.run()["o"], alone) and not torch.equal(few, alone)

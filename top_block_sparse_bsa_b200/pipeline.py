@@ -579,7 +579,7 @@ class QuantDecodeStep(_Replaceable):
             self._bring_up()
         b = self.bufs
         if idx is None:
-            idx = b.get("idx")
+            idx = b["idx"] if self.kb is not None else None
         elif idx.dim() != 3 or idx.shape[0] != self.shape.B or idx.shape[1] != self.shape.Hkv:
             raise ValueError(f"idx is [{self.shape.B}, {self.shape.Hkv}, n], got {list(idx.shape)}")
         bsa_sparse_attn_decode_quant(self.shape, self.q, self.k_pool, self.v_pool, self.k_exp, self.v_exp,
