@@ -153,6 +153,25 @@ def test_replaced_tensors_of_the_same_size_count_from_the_next_call_on(pipe):
     assert torch.equal(step.backward(*grads)["d_qkv"], fresh.backward(*grads)["d_qkv"])
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_gradients_made_on_another_stream_take_no_memory_that_this_one_still_reads(pipe, handle):
+    """The first backward takes memory for its outputs; on another stream it must not be what this stream has given back
+    and its queued work is still to read."""
+    qkv = _qkv(1, 512, 6, 1, 128, torch.bfloat16, spread=0.3).cuda()
+    step = _encode_step(pipe, qkv, 6, 1, (None, None), None, "half", None, 1.0)
+    grads = [torch.ones((1, h, 512, 128), device="cuda") for h in (6, 1, 1)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    x = torch.full_like(qkv, 7.0)
+    torch.cuda._sleep(50_000_000)                            # some 30 ms
+    y = x + 0
+    del x
+    step.backward(*grads, stream=side.cuda_stream if handle else side)
+    torch.cuda.synchronize()
+    assert bool((y == 7).all())
+    assert bool((step.bufs["d_qkv"] == 1).all())
+
+
 # --------------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("Hq,d", [(4, 128), (16, 64)])

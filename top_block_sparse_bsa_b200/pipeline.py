@@ -8,6 +8,7 @@ nothing else.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from dataclasses import dataclass, field
 from typing import Dict, Optional, Tuple
@@ -393,6 +394,16 @@ def _buffer(bufs: Dict[str, torch.Tensor], name: str, shape, dtype, device, zero
         raise ValueError(f"bufs[{name!r}] is {list(shape)}, got {list(bufs[name].shape)}")
 
 
+def _memory_of(stream):
+    """Memory taken inside belongs to the call's stream: taken on the current one it may still be in use there, by work
+    that the call's stream does not wait for."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 class _Replaceable:
     """A step whose fields may be replaced between calls: at the next one they are checked, against the sizes that the
     step was built for, and what is derived from them is derived again (``_derive``)."""
@@ -401,8 +412,9 @@ class _Replaceable:
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_current", False)
 
-    def _bring_up(self):
-        self._derive()
+    def _bring_up(self, stream=None):
+        with _memory_of(stream):
+            self._derive()
         object.__setattr__(self, "_current", True)
 
 
@@ -449,7 +461,7 @@ class QkvStep(_Replaceable):
 
     def run(self, stream=None):
         if not self._current:
-            self._bring_up()
+            self._bring_up(stream)
         b = self.bufs
         bsa_qkv_norm_rope(self.shape, self.qkv, self.q_weight, self.k_weight, self.eps, self.rope, self.positions,
                           b["q"], b["k"], b["v"], stream=stream)
@@ -459,7 +471,7 @@ class QkvStep(_Replaceable):
         """Gradients d_qkv (qkv's type, dense) and, with weights, d_q_weight and d_k_weight (fp32) from fp32 dq, dk,
         dv, as PrefillStep.backward gives them."""
         if not self._current:
-            self._bring_up()
+            self._bring_up(stream)
         B, N, H, d = self.qkv.shape
         for name, g, heads in (("dq", dq, self.Hq), ("dk", dk, self.Hkv), ("dv", dv, self.Hkv)):
             if g.shape != (B, heads, N, d):
@@ -467,14 +479,16 @@ class QkvStep(_Replaceable):
         b = self.bufs
         dev = self.qkv.device
         if "d_qkv" not in b:
-            b["d_qkv"] = torch.empty((B, N, H, d), dtype=self.qkv.dtype, device=dev)
+            with _memory_of(stream):
+                b["d_qkv"] = torch.empty((B, N, H, d), dtype=self.qkv.dtype, device=dev)
         weights = (None, None, None)
         if self.q_weight is not None:
             if "qkv_workspace" not in b:
-                _buffer(b, "d_q_weight", (d,), torch.float32, dev)
-                _buffer(b, "d_k_weight", (d,), torch.float32, dev)
-                b["qkv_workspace"] = torch.empty((bsa_workspace_bytes_norm_rope(self.shape),), dtype=torch.uint8,
-                                                 device=dev)
+                with _memory_of(stream):
+                    _buffer(b, "d_q_weight", (d,), torch.float32, dev)
+                    _buffer(b, "d_k_weight", (d,), torch.float32, dev)
+                    b["qkv_workspace"] = torch.empty((bsa_workspace_bytes_norm_rope(self.shape),), dtype=torch.uint8,
+                                                     device=dev)
             weights = (b["d_q_weight"], b["d_k_weight"], b["qkv_workspace"])
         bsa_qkv_norm_rope_bwd(self.shape, self.qkv, self.q_weight, self.k_weight, self.eps, self.rope, self.positions,
                               dq, dk, dv, b["d_qkv"], *weights, stream=stream)
@@ -542,7 +556,7 @@ class QuantDecodeStep(_Replaceable):
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, new_lens: Optional[torch.Tensor] = None, stream=None):
         """Quantise k_new/v_new [B,Hkv,T,d] (t < new_lens[b]) behind seq_lens[b] tokens; completed blocks are pooled."""
         if not self._current:
-            self._bring_up()
+            self._bring_up(stream)
         s = self.shape
         if k_new.shape != v_new.shape or k_new.shape[:2] != (s.B, s.Hkv) or k_new.shape[3] != s.d:
             raise ValueError(f"new keys and values are [{s.B}, {s.Hkv}, T, {s.d}], got {list(k_new.shape)}")
@@ -555,7 +569,7 @@ class QuantDecodeStep(_Replaceable):
     def read(self, k_out: torch.Tensor, v_out: torch.Tensor, starts: Optional[torch.Tensor] = None, stream=None):
         """Tokens starts[b] + t into row t of k_out/v_out [B,Hkv,T,d] (bf16 or fp32), as far as the sequence goes."""
         if not self._current:
-            self._bring_up()
+            self._bring_up(stream)
         s = self.shape
         if k_out.shape != v_out.shape or k_out.shape[:2] != (s.B, s.Hkv) or k_out.shape[3] != s.d:
             raise ValueError(f"rows read back are [{s.B}, {s.Hkv}, T, {s.d}], got {list(k_out.shape)}")
@@ -566,7 +580,7 @@ class QuantDecodeStep(_Replaceable):
 
     def select(self, stream=None):
         if not self._current:
-            self._bring_up()
+            self._bring_up(stream)
         if self.kb is None:
             raise ValueError("this step attends every block (kb None): there is nothing to select")
         b, s = self.bufs, self.shape
@@ -576,7 +590,7 @@ class QuantDecodeStep(_Replaceable):
 
     def attend(self, idx: Optional[torch.Tensor] = None, stream=None, with_lse: bool = True):
         if not self._current:
-            self._bring_up()
+            self._bring_up(stream)
         b = self.bufs
         if idx is None:
             idx = b["idx"] if self.kb is not None else None
