@@ -444,6 +444,9 @@ typedef struct {
  *   BSA_ROPE_PARTS   by the turns r = original_len * f / (2 pi) that a pair
  *                    makes within original_len: r >= beta_fast keeps f, r <=
  *                    beta_slow divides it by factor, a ramp linear in r between
+ *                    (a model trained with a ramp over the pair's index i
+ *                    between those limits has other frequencies there: pass
+ *                    its own as inv_freq)
  * *scale (optional) receives 0.1 ln(factor) + 1 for PARTS and 1 otherwise: the
  * factor on the rotated values that goes with it (set bsa_rope_t.scale to 1
  * for a model trained without it).
@@ -466,7 +469,9 @@ bsa_status_t bsa_rope_inv_freq(int rot_dim, double base, int scaling, double fac
  *   row of magnitudes past 2^60 or so, or under 2^-60 with eps 0, is out of range.
  * rope: see bsa_rope_t; NULL or BSA_ROPE_NONE: no rotation.
  * positions [B, Nq] int32 (optional): the tokens' positions, any int32; NULL:
- *   0..Nq-1.  Angles are formed to 2^-32 turns at any position.
+ *   0..Nq-1.  An angle is off by at most 2^-26 turns (it is rounded to fp32
+ *   after whole turns are taken off) and |position| 2^-55 turns (the rounding
+ *   of a frequency of at most 1 in 64 bits: 2^-24 at the ends of int32).
  * q [B,Hq,Nq,d], k and v [B,Hkv,Nq,d] (dtype) outputs: fp32 inside, rounded
  *   once.  Outputs must not overlap qkv.
  * Built: BF16 and F32, d a multiple of 8 and at most 256.
@@ -508,8 +513,9 @@ size_t bsa_workspace_bytes_norm_rope(const bsa_shape_t* shape);
  *   one exponent byte e; a value is code * 2^(e-127).  e is the least that
  *   brings the row's largest finite magnitude within 448, kept within
  *   [10, 246]; codes are rounded to nearest, ties to even (at most 2^-4 of the
- *   value off; values under 2^(e-133) have steps of 2^(e-136)).  What is stored
- *   is exact in bf16.  Infinities and NaN are stored as NaN.
+ *   value off; values under 2^(e-133) have steps of 2^(e-136); magnitudes past
+ *   1.75 * 2^127, which e = 246 does not reach, are stored as that).  What is
+ *   stored is exact in bf16.  Infinities and NaN are stored as NaN.
  * k_pool/v_pool [num_pages, Hkv, 64, d] bytes, k_exp/v_exp [num_pages, Hkv, 64]
  *   bytes: distinct arrays, all 16-byte aligned.
  * k_new/v_new [B, Hkv, Nq, d] bf16; seq_lens, block_table, table_stride,
@@ -528,7 +534,9 @@ bsa_status_t bsa_paged_append_quant(const bsa_shape_t* shape, const void* k_new,
 
 /*
  * bsa_paged_read_quant -- tokens of the quantised cache read back as dense
- * rows, e.g. the keys and values in front of a prefill over a cached context.
+ * rows: a cached context for the calls that take a dense bf16 cache
+ * (bsa_sparse_attn_decode and its kin) or for the caller's own attention.  The
+ * prefill calls here take Nq = Nk and read no prefix.
  * Token starts[b] + t of sequence b, t < Nq, becomes row t of k_out/v_out
  * [B, Hkv, Nq, d] (dtype: BF16, exact, or F32; either may be NULL, not both);
  * rows at or past the sequence's length seq_lens[b] are left as they were.
@@ -557,8 +565,15 @@ bsa_status_t bsa_paged_read_quant(const bsa_shape_t* shape, const void* k_pool, 
  *   own length has no keys; an entry >= nb, or a needed table entry outside
  *   [0, num_pages), is skipped and flagged (BSA_DEV_BAD_INDEX).
  * o [B,Hq,d] bf16; lse [B,Hq] fp32 (optional), natural log.  A row without a
- *   key gives o = 0 and lse = -inf.  Value rows whose exponent byte is below 56
- *   (values under 2^-62) enter o with an absolute error of up to 2^-94.
+ *   key gives o = 0 and lse = -inf.
+ * Rounding: logits, the softmax's sum and o's sums are fp32.  A key's weight in
+ *   o's sum (softmax weight times the power of two of its value row) is fp16,
+ *   scaled by the largest: off by at most 2^-11 of itself or 2^-33 of the
+ *   largest one.  A query head's channels are taken to fp16 with the largest (from
+ *   2^-116 on) at 2^10 or above: exact but for channels under 2^-27 of it, which
+ *   are off by at most 2^-35 of it.  Value rows whose exponent byte is below 56 (values
+ *   under 2^-62) enter o with an absolute error of up to 2^-94.  Logits past
+ *   2^95 may become infinite.
  * workspace: bsa_workspace_bytes(BSA_OP_DECODE_QUANT, shape, idx_stride) bytes,
  *   256-byte aligned; its contents on entry do not matter; calls that may
  *   overlap need one each.

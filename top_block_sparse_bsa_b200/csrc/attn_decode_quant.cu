@@ -13,9 +13,9 @@
 // for each of at most 16 heads; the cache's own bytes, read once per KV head
 // for all its query heads, are the floor.  So the design keeps loads in
 // flight and spends few instructions a byte:
-//   - a warp takes 16 keys at a time through stages of its own: asynchronous
-//     copies bring 4 KB two chunks ahead and run on across the rows of its
-//     range; no barrier and no block-wide wait stands in the loop.
+//   - a warp takes 16 keys at a time through two stages of its own: asynchronous
+//     copies bring the next 4 KB while it works on a chunk and run on across the
+//     rows of its range; no barrier and no block-wide wait stands in the loop.
 //   - the codes become fp16 pairs by one conversion each (exact), and the
 //     products run on m16n8k16 matrix instructions with the keys (then the
 //     channels) as the 16 rows and eight query heads as the 8 columns.  The
@@ -29,8 +29,10 @@
 //   - M moves only when some y passes it by 2^7 (one vote a step; M starts at
 //     the first maximum): w is scaled by 2^8, so it stays within fp16 and keeps
 //     its 11 bits down to 2^-22 of the largest.
-// w is rounded to fp16 for the product (at most 2^-11 of w); l sums its terms
-// unrounded; logits, O and l are fp32.
+// w is rounded to fp16 for the product, the matrix unit's type that takes the
+// codes exactly: at most 2^-11 of w, an eighth of the output's own rounding to
+// bf16, or 2^-33 of the largest w.  l sums its terms unrounded; logits, O and l
+// are fp32.
 //
 // Work split: the rows' list positions are laid end to end, each sequence
 // with the blocks it has, and cut into equal ranges, one per team of warps: a
@@ -40,11 +42,14 @@
 // cut by range borders leaves one partial record (M, l, O) per range, at most
 // two a team, and the second kernel joins them.
 //
-// 16 ragged sequences of 8 KV heads, 32 query heads: every block (2.5 GB) 381 to
-// 389 us (96 to 98% of the copy rate, by the clock under the power cap), 97 kept
-// blocks 38.2 us (81%), of which some 4.5 pass before the first keys are there
-// (list, table, keys, one after the other, with cold code) and 1.3 in the join;
-// one sequence of 30000 tokens 18.9 us, of 4001 10.8.
+// 16 ragged sequences of 8 KV heads, 32 query heads: every block (2.5 GB) 382 to
+// 393 us (95 to 98% of the copy rate, by the clock under the power cap), 97 kept
+// blocks 37.1 to 39.0 us (80 to 84%), of which some 4.5 pass before the first
+// keys are there (list, table, keys, one after the other, with cold code) and
+// 1.3 in the join; one sequence of 30000 tokens 17.0 to 18.7 us, of 4001 11.0 to
+// 11.9.  d = 64: every block 201 us (94%), 97 kept blocks 23.3 us (67%).  128
+// query heads: every block 473 to 482 us (78%; d = 64 271 us, 70%), 97 kept
+// blocks 47.8 us (65%).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -715,19 +720,23 @@ cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t st) {
 }  // namespace qdecode
 
 // One team of all warps an SM, or, while there are more rows than teams, two or
-// four smaller ones; two also where rows of unknown lengths number more than half
-// of the SMs (128 rows of 1.5K to 3K tokens 22.1 us, in one team an SM 23.8; 96 of 2K
-// to 6K 25.5 and 26.2): such rows are cut, and one team loads while the other joins.
-// All multiprocessors take part: in short bursts 7/8 of them draw more from memory
-// than all (the whole cache of 16 sequences 371 us against 397), but under steady
-// load, where the power cap lowers the clock, they fall behind (430 us against
-// 405; both before the present join).
+// four smaller ones (33 kept blocks, us: 192 rows in two teams an SM 25.1, in one
+// 28.8; 512 rows in four 52.1, in two 55.9); two also where rows of unknown
+// lengths number more than half of the SMs (128 rows of 1.5K to 3K tokens 22.3 us,
+// in one team an SM 24.4; 96 of 2K to 6K 25.9 and 26.7; at 64 rows they are even,
+// 16.1 and 16.5): such rows are cut, and one team loads while the other joins.
+// All multiprocessors take part (the whole cache of 16 sequences 387 to 390 us, on
+// 7/8 of them 404 to 415).
 // Ranges that end where rows end leave fewer records to join (97 kept blocks,
-// us: 128 rows on 128 ranges 42.3, on 148 45.0; 24 rows on 144 16.0, on 148
-// 19.0): from a list, where rows are equally long, as many ranges a row as fit
-// the teams, or whole rows a range, if that keeps at least 4/5 of the teams busy;
-// without one only where a row has four ranges or more (its own length may be
-// the only one).
+// us: 24 rows on 144 ranges 13.0, on 148 15.9; 48 on 144 18.0 and 21.2; 120 on
+// 120 35.6 and 40.4; 128 on 128 37.3 to 37.9 and 41.1; 33 blocks, 256 rows on 256
+// 27.4, on 296 31.4): from a list, where rows are equally long, as many ranges a
+// row as fit the teams, or whole rows a range, if that keeps at least 4/5 of the
+// teams busy.  With fewer busy it goes either way (80 rows on 80 33.1, on 148
+// 29.2; 160 on 160 24.0, on 296 22.6; but 112 on 112 33.8, on 148 37.1).  Without a
+// list only where a row has four ranges or more (32 rows of 15K to 30K tokens on
+// 128 38.1, on 148 38.7; 8 rows on 144 12.9 and 15.7; 48 rows may gain or lose:
+// its own length may be the only one).
 QuantSplit quant_decode_split(int num_sms, int group, int rows, bool list, int forced) {
   const int NB = group > 8 ? 2 : 1;
   QuantSplit s;

@@ -18,13 +18,16 @@
 // of the norm are shuffles inside the row's lanes.  A lane keeps its channels
 // from head to head, so the cosines and sines of a token are computed once per
 // lane and serve all its heads: no table of angles is read.  32K tokens of 48
-// heads, bf16: 135 us, 91% of the copy rate; fp32 252 us, 97%; the backward of
-// 32K tokens of 36 heads 202 us, 88%.
+// heads, bf16: 134 to 137 us, 89 to 91% of the copy rate; fp32 254 us, 97%; the
+// backward of 32K tokens of 36 heads 204 to 217 us (82 to 88%, by box and
+// clock), with fp32 inputs 273 us, 97%.
 //
 // Angles.  position * inv_freq reaches 1e6 radians and more, where an fp32
 // product is off by 0.06.  The frequency in turns, modulo one, is held as a
 // 64-bit fixed-point fraction; the integer product with the position wraps
-// modulo one turn exactly, and its top 32 bits are the angle to 2^-32 turns.
+// modulo one turn exactly.  What is left: the top 32 bits become an fp32 argument
+// (2^-26 turns), and the frequency's own rounding in 64 bits, 2^-55 turns for
+// frequencies up to 1, grows with the position (2^-24 turns at the ends of int32).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -221,8 +224,9 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // Forward: one block per token tile (kThreads / GS tokens, one per lane group)
 // and run of head_run heads.  Blocks that start as others end do better here
-// than resident ones with even shares (144 us against 181 for 32K tokens: these
-// run in step, all loading or all storing, and the split costs registers).
+// than resident ones with even shares (144 us against 181 for 32K tokens, both in
+// 8-byte pieces: these run in step, all loading or all storing, and the split
+// costs registers).
 template <typename T, int GS, int LAYOUT, int E>
 __global__ void __launch_bounds__(kThreads, fwd_ctas<T, E>()) fwd_kernel(const NormRopeArgs p) {
   griddep_wait();
@@ -357,7 +361,9 @@ struct Range {
 // token and added to the lane's own place in shared memory token by token
 // (which frees half of the registers that sums over all rows would hold); the
 // block's groups are added in order at the end, and dw_reduce_kernel adds the
-// blocks in 64 bits: the same order on every run.
+// blocks in 64 bits: the same order on every run.  Inside a block the sums are
+// fp32: a block sees 1/296 of the rows, and sums in 64 bits would take twice the
+// registers and shared memory of the part that bounds the pass.
 template <typename T, int GS, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) bwd_kernel(const NormRopeArgs p) {
   griddep_wait();
