@@ -11,7 +11,7 @@ from __future__ import annotations
 import contextlib
 import math
 from dataclasses import dataclass, field
-from typing import Dict, Optional, Tuple
+from typing import ClassVar, Dict, Optional, Tuple
 
 import torch
 
@@ -381,7 +381,7 @@ class HssaStep:
         return b
 
 
-def _fits(what: str, t: Optional[torch.Tensor], *shape: int):
+def _fits(what: str, t: Optional[torch.Tensor], shape: Tuple[int, ...]):
     if t is not None and t.shape != shape:
         raise ValueError(f"{what} is {list(shape)}, got {list(t.shape)}")
 
@@ -405,17 +405,26 @@ def _memory_of(stream):
 
 
 class _Replaceable:
-    """A step whose fields may be replaced between calls: at the next one they are checked, against the sizes that the
-    step was built for, and what is derived from them is derived again (``_derive``)."""
+    """A step whose fields may be replaced between calls: at the next one those replaced are checked, against the sizes
+    that the step was built for (``_sizes``), and what is derived from them is derived again (``_derive``)."""
+    _stale: ClassVar[Tuple[str, ...]] = ()
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
-        object.__setattr__(self, "_current", False)
+        if name not in self._stale:
+            object.__setattr__(self, "_stale", self._stale + (name,))
 
     def _bring_up(self, stream=None):
-        with _memory_of(stream):
-            self._derive()
-        object.__setattr__(self, "_current", True)
+        others = []
+        for name in self._stale:
+            size = self._sizes.get(name)
+            if size is None:
+                others.append(name)
+            else:
+                _fits(name, getattr(self, name), size)
+        if others:
+            self._derive(others, stream)
+        object.__setattr__(self, "_stale", ())
 
 
 @dataclass
@@ -444,23 +453,23 @@ class QkvStep(_Replaceable):
         if H != self.Hq + 2 * self.Hkv:
             raise ValueError(f"qkv has {H} heads a token, not {self.Hq} + 2 * {self.Hkv}")
         self.shape = make_shape(B, self.Hq, self.Hkv, N, N, d, 1, self.qkv.dtype)
+        self._sizes = {"qkv": (B, N, H, d), "positions": (B, N), "q_weight": (d,), "k_weight": (d,)}
         self._bring_up()
 
-    def _derive(self):
+    def _derive(self, stale, stream):
         s = self.shape
-        _fits("qkv", self.qkv, s.B, s.Nq, s.Hq + 2 * s.Hkv, s.d)
         if (self.Hq, self.Hkv) != (s.Hq, s.Hkv):
             raise ValueError(f"this step has {s.Hq} query and {s.Hkv} key heads")
-        _fits("positions", self.positions, s.B, s.Nq)
-        _fits("q_weight", self.q_weight, s.d)
-        _fits("k_weight", self.k_weight, s.d)
-        self.rope = make_rope(self.layout if self.inv_freq is not None else BSA_ROPE_NONE, self.inv_freq,
-                              self.rope_scale)
-        for name, heads in (("q", s.Hq), ("k", s.Hkv), ("v", s.Hkv)):
-            _buffer(self.bufs, name, (s.B, heads, s.Nq, s.d), self.qkv.dtype, self.qkv.device)
+        if "inv_freq" in stale or "layout" in stale or "rope_scale" in stale:
+            self.rope = make_rope(self.layout if self.inv_freq is not None else BSA_ROPE_NONE, self.inv_freq,
+                                  self.rope_scale)
+        if "bufs" in stale:
+            with _memory_of(stream):
+                for name, heads in (("q", s.Hq), ("k", s.Hkv), ("v", s.Hkv)):
+                    _buffer(self.bufs, name, (s.B, heads, s.Nq, s.d), self.qkv.dtype, self.qkv.device)
 
     def run(self, stream=None):
-        if not self._current:
+        if self._stale:
             self._bring_up(stream)
         b = self.bufs
         bsa_qkv_norm_rope(self.shape, self.qkv, self.q_weight, self.k_weight, self.eps, self.rope, self.positions,
@@ -470,7 +479,7 @@ class QkvStep(_Replaceable):
     def backward(self, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, stream=None):
         """Gradients d_qkv (qkv's type, dense) and, with weights, d_q_weight and d_k_weight (fp32) from fp32 dq, dk,
         dv, as PrefillStep.backward gives them."""
-        if not self._current:
+        if self._stale:
             self._bring_up(stream)
         B, N, H, d = self.qkv.shape
         for name, g, heads in (("dq", dq, self.Hq), ("dk", dk, self.Hkv), ("dv", dv, self.Hkv)):
@@ -526,17 +535,22 @@ class QuantDecodeStep(_Replaceable):
         self.idx_stride = 0 if self.kb is None else self.kb + 1
         if self.softmax_scale is None:
             self.softmax_scale = 1.0 / math.sqrt(d)
+        self._sizes = {"q": (B, Hq, d), "block_table": (B, nb), "seq_lens": (B,)}
         self._bring_up()
 
-    def _derive(self):
-        s, b, dev, f32 = self.shape, self.bufs, _dev(self.q), torch.float32
-        _fits("q", self.q, s.B, s.Hq, s.d)
-        _fits("k_pool", self.k_pool, self.k_pool.shape[0], s.Hkv, self.block, s.d)
-        _fits("block_table", self.block_table, s.B, self.nb)
-        _fits("seq_lens", self.seq_lens, s.B)
+    def _derive(self, stale, stream):
+        s = self.shape
+        if "k_pool" in stale:      # the other pools are compared with it at every call
+            _fits("k_pool", self.k_pool, (self.k_pool.shape[0], s.Hkv, self.block, s.d))
         if (self.kb is None) != (self.idx_stride == 0) or (self.kb is not None and self.kb >= self.idx_stride):
             raise ValueError(f"this step was built for kb {f'< {self.idx_stride}' if self.idx_stride else 'None'}, "
                              f"got {self.kb}")
+        if "bufs" in stale:
+            with _memory_of(stream):
+                self._buffers()
+
+    def _buffers(self):
+        s, b, dev, f32 = self.shape, self.bufs, _dev(self.q), torch.float32
         if self.idx_stride:
             _buffer(b, "kbar", (s.B, s.Hkv, self.nb, s.d), f32, dev, zero=True)
             _buffer(b, "qbar", (s.B, s.Hkv, s.d), f32, dev)
@@ -555,7 +569,7 @@ class QuantDecodeStep(_Replaceable):
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, new_lens: Optional[torch.Tensor] = None, stream=None):
         """Quantise k_new/v_new [B,Hkv,T,d] (t < new_lens[b]) behind seq_lens[b] tokens; completed blocks are pooled."""
-        if not self._current:
+        if self._stale:
             self._bring_up(stream)
         s = self.shape
         if k_new.shape != v_new.shape or k_new.shape[:2] != (s.B, s.Hkv) or k_new.shape[3] != s.d:
@@ -568,7 +582,7 @@ class QuantDecodeStep(_Replaceable):
 
     def read(self, k_out: torch.Tensor, v_out: torch.Tensor, starts: Optional[torch.Tensor] = None, stream=None):
         """Tokens starts[b] + t into row t of k_out/v_out [B,Hkv,T,d] (bf16 or fp32), as far as the sequence goes."""
-        if not self._current:
+        if self._stale:
             self._bring_up(stream)
         s = self.shape
         if k_out.shape != v_out.shape or k_out.shape[:2] != (s.B, s.Hkv) or k_out.shape[3] != s.d:
@@ -579,7 +593,7 @@ class QuantDecodeStep(_Replaceable):
                              self.v_exp, self.block_table, self.seq_lens, k_out, v_out, starts=starts, stream=stream)
 
     def select(self, stream=None):
-        if not self._current:
+        if self._stale:
             self._bring_up(stream)
         if self.kb is None:
             raise ValueError("this step attends every block (kb None): there is nothing to select")
@@ -589,7 +603,7 @@ class QuantDecodeStep(_Replaceable):
                              self.idx_stride, b["count"], stream=stream)
 
     def attend(self, idx: Optional[torch.Tensor] = None, stream=None, with_lse: bool = True):
-        if not self._current:
+        if self._stale:
             self._bring_up(stream)
         b = self.bufs
         if idx is None:
