@@ -573,7 +573,9 @@ bsa_status_t bsa_paged_read_quant(const bsa_shape_t* shape, const void* k_pool, 
  *   2^-116 on) at 2^10 or above: exact but for channels under 2^-27 of it, which
  *   are off by at most 2^-35 of it.  Value rows whose exponent byte is below 56 (values
  *   under 2^-62) enter o with an absolute error of up to 2^-94.  Logits past
- *   2^95 may become infinite.
+ *   2^95 may become infinite.  lse passes through sums with the value rows'
+ *   exponents: off by a few 2^-24 of their largest magnitude (2^-18 or less for
+ *   values between 2^-30 and 2^30), beside its logits' own errors.
  * workspace: bsa_workspace_bytes(BSA_OP_DECODE_QUANT, shape, idx_stride) bytes,
  *   256-byte aligned; its contents on entry do not matter; calls that may
  *   overlap need one each.

@@ -172,6 +172,29 @@ def test_gradients_made_on_another_stream_take_no_memory_that_this_one_still_rea
     assert bool((step.bufs["d_qkv"] == 1).all())
 
 
+def test_encode_and_backward_past_32_bits(pipe):
+    """More than 2^31 channels: the last tokens come out as in a call of their own."""
+    Hq, Hkv, N, d, tail = 32, 8, 360_000, 128, 70
+    freq, _ = _rope_inputs(d, "half")
+    w = _weights(d, torch.bfloat16, True)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    qkv = torch.randn((1, N, Hq + 2 * Hkv, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    assert qkv.numel() > 2 ** 31
+    pos = torch.arange(N, dtype=torch.int32).view(1, N)
+    step = _encode_step(pipe, qkv, Hq, Hkv, w, freq, "half", pos, 1.0)
+    last = _encode_step(pipe, qkv[:, -tail:].contiguous(), Hq, Hkv, w, freq, "half", pos[:, -tail:].contiguous(), 1.0)
+    got, want = step.run(), last.run()
+    assert all(torch.equal(got[n][:, :, -tail:], want[n]) for n in "qkv")
+    grads = [torch.zeros((1, h, N, d), device="cuda") for h in (Hq, Hkv, Hkv)]      # none but the last tokens'
+    for x in grads:
+        x[:, :, -tail:] = torch.randn((1, x.shape[1], tail, d), generator=g, device="cuda")
+    got, want = step.backward(*grads), last.backward(*(x[:, :, -tail:].contiguous() for x in grads))
+    assert torch.equal(got["d_qkv"][:, -tail:], want["d_qkv"]) and not got["d_qkv"][:, :-tail].any()
+    for name in ("d_q_weight", "d_k_weight"):
+        # the same terms, at most tail * Hq, in sums of another order
+        assert bool(((got[name] - want[name]).abs() <= tail * Hq * 2.0 ** -24 * 2 * want[name].abs().max()).all())
+
+
 # --------------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("Hq,d", [(4, 128), (16, 64)])
