@@ -55,12 +55,6 @@ __host__ __device__ constexpr int bwd_rows() {
 
 enum { LAYOUT_NONE = 0, LAYOUT_HALF = 1, LAYOUT_PAIRS = 2 };
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // E consecutive channels of a row, kept as loaded: a bf16 piece waits for its
 // turn in half of the registers.  pairs() gives them as packed fp32 pairs.
 template <typename T, int E>

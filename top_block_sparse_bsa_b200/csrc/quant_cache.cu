@@ -27,12 +27,6 @@ namespace qcache {
 constexpr int kThreads = 256;          // reads
 constexpr int kAppendThreads = 128;
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Exponent byte of a row whose largest finite magnitude is m.
 __device__ __forceinline__ uint32_t exponent_byte(float m) {
   const uint32_t u = __float_as_uint(m);
