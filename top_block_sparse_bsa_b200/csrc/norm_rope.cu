@@ -19,7 +19,7 @@
 // from head to head, so the cosines and sines of a token are computed once per
 // lane and serve all its heads: no table of angles is read.  32K tokens of 48
 // heads, bf16: 134 to 137 us, 89 to 91% of the copy rate; fp32 254 us, 97%; the
-// backward of 32K tokens of 36 heads 204 to 217 us (82 to 88%, by box and
+// backward of 32K tokens of 36 heads 204 to 218 us (82 to 88%, by box and
 // clock), with fp32 inputs 273 us, 97%.
 //
 // Angles.  position * inv_freq reaches 1e6 radians and more, where an fp32
