@@ -195,6 +195,21 @@ def test_encode_and_backward_past_32_bits(pipe):
         assert bool(((got[name] - want[name]).abs() <= tail * Hq * 2.0 ** -24 * 2 * want[name].abs().max()).all())
 
 
+@pytest.mark.parametrize("brought", [(), ("qkv_workspace",), ("d_q_weight",), ("d_k_weight", "qkv_workspace"), ("d_qkv",)])
+def test_backward_makes_the_buffers_that_the_caller_did_not_bring(pipe, brought):
+    qkv = _qkv(1, 70, 3, 1, 64, torch.bfloat16, spread=0.5).cuda()
+    w = _weights(64, torch.bfloat16, True)
+    freq, _ = _rope_inputs(64, "half")
+    grads = [torch.randn((1, h, 70, 64), generator=torch.Generator().manual_seed(h)).cuda() for h in (3, 1, 1)]
+    want = _encode_step(pipe, qkv, 3, 1, w, freq, "half", None, 1.0).backward(*grads)
+    bufs = {n: torch.empty_like(want[n]) for n in brought}
+    step = pipe.QkvStep(qkv, 3, 1, q_weight=w[0].cuda(), k_weight=w[1].cuda(), eps=1e-5, inv_freq=freq.cuda(),
+                        bufs=dict(bufs))
+    got = step.backward(*grads)
+    assert all(torch.equal(got[n], want[n]) for n in ("d_qkv", "d_q_weight", "d_k_weight"))
+    assert all(got[n] is bufs[n] for n in brought)
+
+
 # --------------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("Hq,d", [(4, 128), (16, 64)])

@@ -76,3 +76,12 @@ def test_decode_step_refuses_small_buffers_and_a_late_kb():
     step.kb = 2
     with pytest.raises(ValueError):
         step.select()
+
+
+def test_encode_step_refuses_small_gradient_buffers_that_come_with_a_workspace():
+    for small in ("d_q_weight", "d_k_weight"):
+        bufs = {"d_q_weight": torch.zeros(64), "d_k_weight": torch.zeros(64), "qkv_workspace": torch.zeros(1024, dtype=U8)}
+        bufs[small] = torch.zeros(32)
+        step = _encode(bufs=bufs)
+        with pytest.raises(ValueError):
+            step.backward(*[torch.zeros((2, h, 3, 64)) for h in (4, 2, 2)])

@@ -492,13 +492,16 @@ class QkvStep(_Replaceable):
                 b["d_qkv"] = torch.empty((B, N, H, d), dtype=self.qkv.dtype, device=dev)
         weights = (None, None, None)
         if self.q_weight is not None:
-            if "qkv_workspace" not in b:
+            if "d_q_weight" not in b or "d_k_weight" not in b or "qkv_workspace" not in b:
                 with _memory_of(stream):
                     _buffer(b, "d_q_weight", (d,), torch.float32, dev)
                     _buffer(b, "d_k_weight", (d,), torch.float32, dev)
-                    b["qkv_workspace"] = torch.empty((bsa_workspace_bytes_norm_rope(self.shape),), dtype=torch.uint8,
-                                                     device=dev)
+                    if "qkv_workspace" not in b:
+                        b["qkv_workspace"] = torch.empty((bsa_workspace_bytes_norm_rope(self.shape),),
+                                                         dtype=torch.uint8, device=dev)
             weights = (b["d_q_weight"], b["d_k_weight"], b["qkv_workspace"])
+            if weights[0].numel() < d or weights[1].numel() < d:
+                raise ValueError(f"bufs['d_q_weight'] and bufs['d_k_weight'] are [{d}]")
         bsa_qkv_norm_rope_bwd(self.shape, self.qkv, self.q_weight, self.k_weight, self.eps, self.rope, self.positions,
                               dq, dk, dv, b["d_qkv"], *weights, stream=stream)
         return b
